@@ -726,6 +726,189 @@ int pulse_encode_noalloc(const float *master_f32, uint16_t *prev_bf16, uint64_t 
                          uint32_t *idx_out, uint16_t *val_out, uint64_t *count_out,
                          cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Optimizer step. [TALK] 07:24-09:09 and [PULSE] "Osservazione Centrale" start
+ * from the FP32 master weights that one Adam step has moved; these entry
+ * points are that step: the global gradient norm with its clip factor, and
+ * AdamW (decoupled weight decay) over every tensor of a model in one launch,
+ * with FP32 moments or with 8-bit ones. pulse_encode_multi then reads the
+ * same master buffers.
+ *
+ * One step, for every element, every operation one FP32 operation rounded to
+ * nearest unless noted:
+ *   g = gradient * grad_scale                  (grad_scale NULL: g = gradient)
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * g) * (1 - beta2)
+ *   w = w - (a * m / (sqrt(v) * s + eps) + w * d)
+ *   a = lr * lr_scale / (1 - beta1^step),  s = 1 / sqrt(1 - beta2^step),
+ *   d = lr * lr_scale * weight_decay
+ * m and v are reproducible bit for bit (no fused multiply-add); the quotient
+ * and the square root in w may be off by a few units in the last place of the
+ * update. A grad_scale that is not finite leaves w, m and v as they are (the
+ * step of a step's non-finite gradients is skipped without a host round trip).
+ *
+ * 8-bit moments. Blocks of 256 consecutive elements of a tensor (the last may
+ * be shorter) share one exponent byte per moment. With E the FP32 exponent
+ * field of the block's largest magnitude, limited to [15, 253] for m and
+ * [31, 253] for v, a code is
+ *   m: bit 7 the sign, bits 0-6 c;  value 0 if c = 0, else +-FP32 bits (8 (E - 14) + c) << 20
+ *   v: bits 0-7 c;                  value 0 if c = 0, else   FP32 bits (8 (E - 30) + c) << 20
+ * that is 3 mantissa bits over 16 (m) or 32 (v) binades, one of them above the
+ * block's maximum so that rounding up has room. Encoding rounds
+ * stochastically: 16 random bits r are added at the top of the 20 dropped
+ * mantissa bits, c = clamp(((bits + (r << 4)) >> 20) - base, 0, max). The mean
+ * of a rounded value is the value, which nearest rounding would not give: with
+ * beta2 = 0.999 one step moves v by less than half a code step and v would
+ * never move. A v above 0 is kept at c >= 1, so that no m is divided by eps
+ * alone. A block that holds a NaN or an infinity gets exponent byte 0xFF and
+ * codes 0x7F and reads as NaN.
+ *   r: h = mix(key + j * 0x9E3779B9), j the place in the block; m takes the
+ *   upper 16 bits of h, v the lower; key = mix(k0 ^ mix(lo(b) ^ mix(hi(b)))), b
+ *   the block's number in the plan (each tensor starts a new block); k0 = the
+ *   fold x = mix(x + word + 0x9E3779B9) from 0 over lo(seed), hi(seed),
+ *   lo(step), hi(step); mix(x): x ^= x >> 16; x *= 0xBB67AE85; x ^= x >> 15;
+ *   x *= 0x9E3779B9; x ^= x >> 16 (uint32).
+ * Zero bytes everywhere are a valid fresh state (m = v = 0).
+ * ---------------------------------------------------------------------- */
+#define PULSE_F32  0  /* element type FP32 */
+#define PULSE_BF16 1  /* element type BF16 */
+#define PULSE_ADAM_BLOCK 256
+
+typedef struct pulse_adam_tensor {
+  uint64_t n;          /* elements (0 allowed) */
+  float *master;       /* n floats, in/out; NULL in a plan only used for the norm */
+  const void *grad;    /* n elements of grad_dtype; NULL: no gradient, the tensor is left alone */
+  int grad_dtype;      /* PULSE_F32 or PULSE_BF16 */
+  void *m;             /* n floats, or n code bytes */
+  void *v;             /* n floats, or n code bytes */
+  uint8_t *m_exp;      /* 8-bit moments: ceil(n / 256) exponent bytes; else NULL */
+  uint8_t *v_exp;
+  float *m_out;        /* 8-bit moments: n floats for pulse_adam_export_multi, or NULL */
+  float *v_out;
+  float weight_decay;  /* finite, >= 0 */
+  float lr_scale;      /* finite, >= 0: this tensor's factor on lr */
+} pulse_adam_tensor;
+
+typedef struct pulse_adam_hyper {
+  uint64_t step;       /* 1 for the first step */
+  uint64_t seed;       /* of the stochastic rounding (8-bit moments) */
+  double lr;           /* finite, >= 0 */
+  double beta1, beta2; /* in [0, 1) */
+  double eps;          /* >= 2^-126, finite */
+} pulse_adam_hyper;
+
+typedef struct pulse_adam_plan pulse_adam_plan;
+
+/*
+ * pulse_adam_plan_create -- tables of a model's tensors, built once ([PPLX]).
+ * state_bits: 32 or 8. The plan keeps the pointers, not the buffers. Calls on
+ * one plan share its workspace: order them (one stream, or events).
+ * Errors: PULSE_ERR_INVALID (ntensors outside [1, 16384], an unknown type, a
+ * weight_decay or lr_scale out of range, an FP32 pointer off 4 bytes or a BF16
+ * one off 2), PULSE_ERR_RANGE (n >= 2^32), PULSE_ERR_NOMEM, PULSE_ERR_CUDA.
+ */
+int pulse_adam_plan_create(const pulse_adam_tensor *tensors, int ntensors, int state_bits,
+                           pulse_adam_plan **plan_out);
+int pulse_adam_plan_destroy(pulse_adam_plan *plan); /* synchronises the device; NULL is fine */
+
+/* New gradient pointers (host array of ntensors device pointers, NULL entries
+ * as in the plan; the types stay), copied before the call returns and used by
+ * work that is enqueued on `stream` after it. */
+int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
+                              cudaStream_t stream);
+
+/*
+ * pulse_grad_norm_multi -- norm_out[0] = sqrt(sum of the squares of every
+ * gradient of the plan); clip_out[0] = min(1, max_norm / (norm + 1e-6)), or NaN
+ * where the norm is not finite, so that a step given clip_out as grad_scale is
+ * skipped. Squares are summed in FP32 over at most 64 elements and in FP64 from
+ * there on, in an order that depends on sizes alone: the same gradients give
+ * the same bits. Gradients above about 1e18 overflow to an infinite norm.
+ *   norm_out, clip_out  device, one float each; clip_out may be NULL
+ *   max_norm            >= 0 (infinity: never clips)
+ */
+int pulse_grad_norm_multi(pulse_adam_plan *plan, float max_norm, float *norm_out, float *clip_out,
+                          cudaStream_t stream);
+
+/* One AdamW step over every tensor that has a gradient. grad_scale: device,
+ * one float, or NULL. Errors: PULSE_ERR_INVALID (also a plan in which a tensor
+ * with n > 0 lacks master, m or v, or the exponent bytes of 8-bit moments). */
+int pulse_adam_step_multi(pulse_adam_plan *plan, const pulse_adam_hyper *hyper,
+                          const float *grad_scale, cudaStream_t stream);
+
+/* 8-bit moments as the FP32 values they stand for, into m_out and v_out of
+ * every tensor that has them (a checkpoint, a switch to FP32 moments).
+ * PULSE_ERR_INVALID for a plan with FP32 moments. */
+int pulse_adam_export_multi(pulse_adam_plan *plan, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Logit shaping: what a sampler does to a row of logits before it draws a
+ * token, and the gradient of that with respect to the raw logits, for a
+ * trainer that takes its loss at the distribution the rollout was drawn from.
+ * The weights that a patch updates produce the logits; nothing on the pages
+ * describes this step.
+ *
+ * For row r and token t, in FP32, one operation after the other:
+ *   x = logits[r][t]
+ *   t in the row's history:      x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *   c = times t was generated:   x = x - frequency[r] * c;  if c > 0: x = x - presence[r]
+ *   t in the row's bias list:    x = x + its value (of a token listed twice, the last entry's)
+ *   y = x * (1 / temperature[r]) (a temperature that is not above 0: y = x)
+ *   mask bit of t clear:         y = -infinity, whatever x was
+ * out[r][t] = y, rounded to the output type. Backward, with d the gradient of y:
+ *   dx = d / temperature[r];  t in the history: dx = logits[r][t] > 0 ? dx / repetition[r] : dx * repetition[r]
+ *   mask bit of t clear: dx = 0, whatever d was.
+ * A row whose mask allows nothing is all -infinity and has a zero gradient.
+ *
+ * Every pointer may be NULL: the step it belongs to is then left out. History
+ * of row r: tokens[begin[r] .. end[r]), generated from split[r] on (split NULL:
+ * all of it generated). Rows may share or overlap ranges, as the positions of
+ * one training sequence do. Nothing is kept between calls.
+ * ---------------------------------------------------------------------- */
+typedef struct pulse_logits_shaping {
+  uint64_t vocab;            /* columns, in [1, 2^31) */
+  const int32_t *tokens;     /* ntokens token numbers */
+  uint64_t ntokens;
+  const int64_t *begin;      /* per row; required with tokens */
+  const int64_t *split;      /* per row, begin <= split <= end */
+  const int64_t *end;        /* per row; required with tokens */
+  const float *repetition;   /* per row, > 0 */
+  const float *presence;     /* per row */
+  const float *frequency;    /* per row */
+  const float *temperature;  /* per row */
+  const int32_t *bias_tokens;  /* nbias token numbers */
+  const float *bias_values;    /* nbias values */
+  uint64_t nbias;              /* < 2^31 */
+  const int64_t *bias_begin;   /* rows + 1 entries: row r has [bias_begin[r], bias_begin[r + 1]) */
+  const uint32_t *mask;      /* mask_rows rows of mask_stride words: bit t & 31 of word t >> 5 allows token t */
+  uint64_t mask_rows;
+  uint64_t mask_stride;      /* >= ceil(vocab / 32) */
+  const int32_t *mask_row;   /* per row: its mask row, below 0 for none; NULL: row r has mask row r */
+} pulse_logits_shaping;
+
+/*
+ * pulse_logits_shape -- rows of logits, `stride` elements apart (>= vocab), to
+ * out. (in_type, out_type): (F32, F32), (BF16, BF16) or (BF16, F32). out may be
+ * logits itself (same type and stride); any other overlap is refused.
+ * A token number outside [0, vocab), a range outside its list or a mask row
+ * past mask_rows is left out and recorded as PULSE_ERR_INDEX for
+ * pulse_get_error(stream). rows == 0 launches nothing.
+ */
+int pulse_logits_shape(const pulse_logits_shaping *shaping, uint64_t rows, const void *logits,
+                       uint64_t stride, int in_type, void *out, uint64_t out_stride, int out_type,
+                       cudaStream_t stream);
+
+/*
+ * pulse_logits_shape_backward -- dout (rows x vocab, out_type) to dlogits
+ * (in_type). logits are the raw ones that the forward call read (in_type); they
+ * may be NULL where repetition or tokens is. dlogits may be dout itself (same
+ * type and stride). Errors as above.
+ */
+int pulse_logits_shape_backward(const pulse_logits_shaping *shaping, uint64_t rows,
+                                const void *dout, uint64_t dout_stride, int out_type,
+                                const void *logits, uint64_t stride, int in_type, void *dlogits,
+                                uint64_t dlogits_stride, cudaStream_t stream);
+
 /*
  * Test hook for the look-back watchdog (not for production use). Runs
  * pulse_encode with a wait limit of `wait_limit_ns` nanoseconds while tile 0

@@ -5,6 +5,7 @@
 // seconds", section "Statyczny harmonogram", and the CPU-prepared tiling and
 // address map of the humansand.ai summary, section "Pipeline'i GPU'lara
 // tasimak").
+#include <cmath>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -389,6 +390,20 @@ struct pulse_mx_plan {
   ByteSegment* segs = nullptr;      // device, 2 x ntensors: codes then scales of each tensor
   uint64_t* counts = nullptr;       // device, 2 x ntensors (host-count apply staging)
   Workspace ws;
+};
+
+struct pulse_adam_plan {
+  int device = 0;
+  int ntensors = 0;
+  int state_bits = 32;
+  uint64_t total_tiles = 0;
+  bool can_step = false;
+  std::vector<AdamTensorDesc> host_desc;
+  AdamTensorDesc* desc = nullptr;     // device copy
+  AdamTensorDesc* staging = nullptr;  // pinned copy that pulse_adam_plan_set_grads sends
+  cudaEvent_t staged = nullptr;       // the last copy out of `staging`
+  uint32_t* tile_tensor = nullptr;    // device: tensor of each tile
+  double* partials = nullptr;         // device: norm partial sums, then the ticket word
 };
 
 extern "C" {
@@ -1491,6 +1506,310 @@ int pulse_mx_plan_get_error(pulse_mx_plan* plan) {
   if (plan == nullptr) return PULSE_ERR_INVALID;
   if (cudaDeviceSynchronize() != cudaSuccess) return PULSE_ERR_CUDA;
   return workspace_take_error(plan->ws, nullptr);
+}
+
+// ------------------------------------------------------------ optimizer step
+
+namespace {
+
+bool grad_pointer_ok(const void* g, int type) { return aligned(g, type == PULSE_BF16 ? 2 : 4); }
+
+bool adam_tensor_ok(const pulse_adam_tensor& t, int state_bits) {
+  if (t.grad_dtype != PULSE_F32 && t.grad_dtype != PULSE_BF16) return false;
+  if (!(std::isfinite(t.weight_decay) && t.weight_decay >= 0.0f)) return false;
+  if (!(std::isfinite(t.lr_scale) && t.lr_scale >= 0.0f)) return false;
+  if (!aligned(t.master, 4) || !grad_pointer_ok(t.grad, t.grad_dtype)) return false;
+  if (!aligned(t.m_out, 4) || !aligned(t.v_out, 4)) return false;
+  return state_bits == 8 || (aligned(t.m, 4) && aligned(t.v, 4));
+}
+
+AdamTensorDesc make_adam_desc(const pulse_adam_tensor& t, uint64_t tile_begin, uint64_t block_begin) {
+  AdamTensorDesc d{};
+  d.w = t.master;
+  d.g = t.grad;
+  d.m = t.m;
+  d.v = t.v;
+  d.m_exp = t.m_exp;
+  d.v_exp = t.v_exp;
+  d.m_out = t.m_out;
+  d.v_out = t.v_out;
+  d.n = t.n;
+  d.tile_begin = tile_begin;
+  d.block_begin = block_begin;
+  d.weight_decay = t.weight_decay;
+  d.lr_scale = t.lr_scale;
+  d.grad_bf16 = t.grad_dtype == PULSE_BF16 ? 1u : 0u;
+  return d;
+}
+
+int adam_plan_tables(pulse_adam_plan* p, const std::vector<uint32_t>& tile_tensor) {
+  const size_t desc_bytes = sizeof(AdamTensorDesc) * p->host_desc.size();
+  const size_t tile_bytes = sizeof(uint32_t) * (tile_tensor.empty() ? 1 : tile_tensor.size());
+  const size_t part_bytes = sizeof(double) * size_t(kNormMaxCtas) + sizeof(uint64_t);
+  if (cudaMalloc(&p->desc, desc_bytes) != cudaSuccess ||
+      cudaMalloc(&p->tile_tensor, tile_bytes) != cudaSuccess ||
+      cudaMalloc(&p->partials, part_bytes) != cudaSuccess ||
+      cudaMallocHost(&p->staging, desc_bytes) != cudaSuccess)
+    return PULSE_ERR_NOMEM;
+  if (cudaEventCreateWithFlags(&p->staged, cudaEventDisableTiming) != cudaSuccess ||
+      cudaMemcpy(p->desc, p->host_desc.data(), desc_bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
+      (!tile_tensor.empty() &&
+       cudaMemcpy(p->tile_tensor, tile_tensor.data(), sizeof(uint32_t) * tile_tensor.size(),
+                  cudaMemcpyHostToDevice) != cudaSuccess) ||
+      cudaMemset(p->partials, 0, part_bytes) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess)
+    return PULSE_ERR_CUDA;
+  return PULSE_OK;
+}
+
+}  // namespace
+
+int pulse_adam_plan_create(const pulse_adam_tensor* tensors, int ntensors, int state_bits,
+                           pulse_adam_plan** plan_out) {
+  if (plan_out == nullptr) return PULSE_ERR_INVALID;
+  *plan_out = nullptr;
+  if (tensors == nullptr || ntensors < 1 || ntensors > kMaxTensorsPerApplyLaunch)
+    return PULSE_ERR_INVALID;
+  if (state_bits != 32 && state_bits != 8) return PULSE_ERR_INVALID;
+  uint64_t tiles = 0;
+  for (int i = 0; i < ntensors; ++i) {
+    if (tensors[i].n > kMaxElems) return PULSE_ERR_RANGE;
+    if (!adam_tensor_ok(tensors[i], state_bits)) return PULSE_ERR_INVALID;
+    tiles += div_up(tensors[i].n, kAdamTile);
+  }
+  if (tiles > kMaxTiles) return PULSE_ERR_RANGE;
+  pulse_adam_plan* p = new (std::nothrow) pulse_adam_plan();
+  if (p == nullptr) return PULSE_ERR_NOMEM;
+  p->ntensors = ntensors;
+  p->state_bits = state_bits;
+  p->total_tiles = tiles;
+  p->can_step = true;
+  int st = cudaGetDevice(&p->device) == cudaSuccess ? PULSE_OK : PULSE_ERR_CUDA;
+  if (st == PULSE_OK) {
+    try {
+      std::vector<uint32_t> tile_tensor;
+      tile_tensor.reserve(size_t(tiles));
+      p->host_desc.reserve(size_t(ntensors));
+      uint64_t blocks = 0;
+      for (int i = 0; i < ntensors; ++i) {
+        const pulse_adam_tensor& t = tensors[i];
+        p->host_desc.push_back(make_adam_desc(t, tile_tensor.size(), blocks));
+        tile_tensor.insert(tile_tensor.end(), size_t(div_up(t.n, kAdamTile)), uint32_t(i));
+        blocks += div_up(t.n, kAdamBlock);
+        if (t.n > 0)
+          p->can_step = p->can_step && t.master && t.m && t.v &&
+                        (state_bits == 32 || (t.m_exp && t.v_exp));
+      }
+      st = adam_plan_tables(p, tile_tensor);
+    } catch (const std::bad_alloc&) {
+      st = PULSE_ERR_NOMEM;
+    }
+  }
+  if (st != PULSE_OK) {
+    pulse_adam_plan_destroy(p);
+    return st;
+  }
+  *plan_out = p;
+  return PULSE_OK;
+}
+
+int pulse_adam_plan_destroy(pulse_adam_plan* plan) {
+  if (plan == nullptr) return PULSE_OK;
+  const cudaError_t e = cudaDeviceSynchronize();
+  if (plan->desc) cudaFree(plan->desc);
+  if (plan->tile_tensor) cudaFree(plan->tile_tensor);
+  if (plan->partials) cudaFree(plan->partials);
+  if (plan->staging) cudaFreeHost(plan->staging);
+  if (plan->staged) cudaEventDestroy(plan->staged);
+  delete plan;
+  return cuda_status(e);
+}
+
+int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, cudaStream_t stream) {
+  if (plan == nullptr || grads == nullptr) return PULSE_ERR_INVALID;
+  for (int i = 0; i < plan->ntensors; ++i)
+    if (!grad_pointer_ok(grads[i], plan->host_desc[size_t(i)].grad_bf16 ? PULSE_BF16 : PULSE_F32))
+      return PULSE_ERR_INVALID;
+  for (int i = 0; i < plan->ntensors; ++i) plan->host_desc[size_t(i)].g = grads[i];
+  // the copy before this one has left the pinned buffer
+  if (cudaEventSynchronize(plan->staged) != cudaSuccess) return PULSE_ERR_CUDA;
+  const size_t bytes = sizeof(AdamTensorDesc) * plan->host_desc.size();
+  std::memcpy(plan->staging, plan->host_desc.data(), bytes);
+  if (cudaMemcpyAsync(plan->desc, plan->staging, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
+    return PULSE_ERR_CUDA;
+  return cuda_status(cudaEventRecord(plan->staged, stream));
+}
+
+int pulse_grad_norm_multi(pulse_adam_plan* plan, float max_norm, float* norm_out, float* clip_out,
+                          cudaStream_t stream) {
+  if (plan == nullptr || norm_out == nullptr || !(max_norm >= 0.0f)) return PULSE_ERR_INVALID;
+  return cuda_status(launch_grad_norm(plan->desc, plan->tile_tensor, plan->total_tiles,
+                                      sm_count(plan->device), plan->partials,
+                                      reinterpret_cast<uint32_t*>(plan->partials + kNormMaxCtas),
+                                      max_norm, norm_out, clip_out, stream));
+}
+
+int pulse_adam_step_multi(pulse_adam_plan* plan, const pulse_adam_hyper* h, const float* grad_scale,
+                          cudaStream_t stream) {
+  if (plan == nullptr || h == nullptr || !plan->can_step || h->step < 1) return PULSE_ERR_INVALID;
+  if (!(std::isfinite(h->lr) && h->lr >= 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
+      !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(std::isfinite(h->eps) && h->eps >= 0x1p-126))
+    return PULSE_ERR_INVALID;
+  if (plan->total_tiles == 0) return PULSE_OK;
+  const double t = double(h->step);
+  AdamLaunch a{};
+  a.tensors = plan->desc;
+  a.tile_tensor = plan->tile_tensor;
+  a.total_tiles = plan->total_tiles;
+  a.grad_scale = grad_scale;
+  a.alpha = float(h->lr / (1.0 - std::pow(h->beta1, t)));
+  a.lr = float(h->lr);
+  a.beta1 = float(h->beta1);
+  a.one_minus_beta1 = float(1.0 - h->beta1);
+  a.beta2 = float(h->beta2);
+  a.one_minus_beta2 = float(1.0 - h->beta2);
+  a.inv_sqrt_bc2 = float(1.0 / std::sqrt(1.0 - std::pow(h->beta2, t)));
+  a.eps = float(h->eps);
+  a.key = adam_key(h->seed, h->step);
+  return cuda_status(plan->state_bits == 8 ? launch_adam8(a, stream) : launch_adam32(a, stream));
+}
+
+int pulse_adam_export_multi(pulse_adam_plan* plan, cudaStream_t stream) {
+  if (plan == nullptr || plan->state_bits != 8 || !plan->can_step) return PULSE_ERR_INVALID;
+  if (plan->total_tiles == 0) return PULSE_OK;
+  return cuda_status(launch_adam_export(plan->desc, plan->tile_tensor, plan->total_tiles, stream));
+}
+
+// ------------------------------------------------------------ logit shaping
+
+namespace {
+
+uint64_t elem_bytes(int type) { return type == PULSE_BF16 ? 2u : 4u; }
+
+bool types_ok(int in_type, int out_type) {
+  return (in_type == PULSE_F32 && out_type == PULSE_F32) ||
+         (in_type == PULSE_BF16 && (out_type == PULSE_BF16 || out_type == PULSE_F32));
+}
+
+struct RowsOf {
+  const void* p;
+  uint64_t stride;  // elements
+  int type;
+};
+
+// True if some byte belongs to a row of both. Rows of one pitch may lie
+// between one another's (two column ranges of one matrix).
+bool rows_overlap(const RowsOf& a, const RowsOf& b, uint64_t rows, uint64_t vocab) {
+  const uint64_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t wa = vocab * elem_bytes(a.type), wb = vocab * elem_bytes(b.type);
+  const uint64_t sa = a.stride * elem_bytes(a.type), sb = b.stride * elem_bytes(b.type);
+  if (pa >= pb + (rows - 1) * sb + wb || pb >= pa + (rows - 1) * sa + wa) return false;
+  if (sa != sb) return true;
+  const uint64_t off = pb >= pa ? (pb - pa) % sa : (sa - (pa - pb) % sa) % sa;  // of b past a row of a
+  return !(off >= wa && sa - off >= wb);
+}
+
+bool same_rows(const RowsOf& a, const RowsOf& b) {
+  return a.p == b.p && a.stride == b.stride && a.type == b.type;
+}
+
+bool shaping_ok(const pulse_logits_shaping* s) {
+  if (s == nullptr || s->vocab < 1 || s->vocab >= (1ull << 31)) return false;
+  if (s->tokens && (s->begin == nullptr || s->end == nullptr || s->ntokens >= (1ull << 62))) return false;
+  if (s->bias_tokens && (s->bias_values == nullptr || s->bias_begin == nullptr || s->nbias >= (1ull << 31)))
+    return false;
+  return !s->mask || (s->mask_stride >= div_up(s->vocab, 32) && s->mask_rows < (1ull << 62));
+}
+
+bool rows_ok(const RowsOf& r, uint64_t vocab) {
+  return r.p != nullptr && r.stride >= vocab && r.stride < (1ull << 40) &&
+         aligned(r.p, uintptr_t(elem_bytes(r.type)));
+}
+
+// Fills the shaping's part and the stream's error word.
+int logits_args(const pulse_logits_shaping& s, uint64_t rows, cudaStream_t stream, LogitsArgs* a, int* sms) {
+  // one CTA per slice of a row: the grid has to fit its 31 bits
+  if (rows > kMaxTiles / div_up(s.vocab, 1024)) return PULSE_ERR_RANGE;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
+  *sms = sm_count(device);
+  {
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    Workspace* ws = stream_workspace(device, stream);
+    if (ws == nullptr) return PULSE_ERR_NOMEM;
+    const int st = workspace_reserve(*ws, 0, stream);
+    if (st != PULSE_OK) return st;
+    a->error_word = ws->counters + 2;
+  }
+  a->rows = rows;
+  a->vocab = uint32_t(s.vocab);
+  a->tokens = s.tokens;
+  a->ntokens = int64_t(s.ntokens);
+  a->begin = s.begin;
+  a->split = s.split;
+  a->end = s.end;
+  a->repetition = s.repetition;
+  a->presence = s.presence;
+  a->frequency = s.frequency;
+  a->temperature = s.temperature;
+  a->bias_tokens = s.bias_tokens;
+  a->bias_values = s.bias_values;
+  a->nbias = int64_t(s.nbias);
+  a->bias_begin = s.bias_begin;
+  a->mask = s.mask;
+  a->mask_rows = int64_t(s.mask_rows);
+  a->mask_stride = s.mask_stride;
+  a->mask_row = s.mask_row;
+  return PULSE_OK;
+}
+
+}  // namespace
+
+int pulse_logits_shape(const pulse_logits_shaping* shaping, uint64_t rows, const void* logits,
+                       uint64_t stride, int in_type, void* out, uint64_t out_stride, int out_type,
+                       cudaStream_t stream) {
+  if (!shaping_ok(shaping) || !types_ok(in_type, out_type)) return PULSE_ERR_INVALID;
+  if (rows == 0) return PULSE_OK;
+  if (rows > kMaxTiles) return PULSE_ERR_RANGE;
+  const RowsOf src{logits, stride, in_type}, dst{out, out_stride, out_type};
+  if (!rows_ok(src, shaping->vocab) || !rows_ok(dst, shaping->vocab)) return PULSE_ERR_INVALID;
+  if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
+  LogitsArgs a{};
+  int sms = 0;
+  const int st = logits_args(*shaping, rows, stream, &a, &sms);
+  if (st != PULSE_OK) return st;
+  a.src = logits;
+  a.src_stride = stride;
+  a.dst = out;
+  a.dst_stride = out_stride;
+  return cuda_status(launch_logits_shape(a, in_type, out_type, sms, stream));
+}
+
+int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t rows, const void* dout,
+                                uint64_t dout_stride, int out_type, const void* logits,
+                                uint64_t stride, int in_type, void* dlogits,
+                                uint64_t dlogits_stride, cudaStream_t stream) {
+  if (!shaping_ok(shaping) || !types_ok(in_type, out_type)) return PULSE_ERR_INVALID;
+  if (rows == 0) return PULSE_OK;
+  if (rows > kMaxTiles) return PULSE_ERR_RANGE;
+  const bool needs_raw = shaping->tokens && shaping->repetition;
+  const RowsOf src{dout, dout_stride, out_type}, raw{logits, stride, in_type};
+  const RowsOf dst{dlogits, dlogits_stride, in_type};
+  if (!rows_ok(src, shaping->vocab) || !rows_ok(dst, shaping->vocab)) return PULSE_ERR_INVALID;
+  if (needs_raw && (!rows_ok(raw, shaping->vocab) || rows_overlap(raw, dst, rows, shaping->vocab)))
+    return PULSE_ERR_INVALID;
+  if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
+  LogitsArgs a{};
+  int sms = 0;
+  const int st = logits_args(*shaping, rows, stream, &a, &sms);
+  if (st != PULSE_OK) return st;
+  a.src = dout;
+  a.src_stride = dout_stride;
+  a.raw = needs_raw ? logits : nullptr;
+  a.raw_stride = stride;
+  a.dst = dlogits;
+  a.dst_stride = dlogits_stride;
+  return cuda_status(launch_logits_backward(a, in_type, out_type, sms, stream));
 }
 
 }  // extern "C"

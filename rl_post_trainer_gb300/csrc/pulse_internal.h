@@ -345,6 +345,90 @@ cudaError_t launch_xor_apply(const TensorDesc& one, const TensorDesc* tensors,
                              const uint64_t* tile_begin, int ntensors, uint64_t total_tiles,
                              bool multi, int grid, cudaStream_t stream);
 
+// ---------------------------------------------------------------- AdamW step
+constexpr int kAdamBlock = 256;      // elements sharing an exponent byte (8-bit moments)
+constexpr int kAdamThreads = 256;
+constexpr int kAdamTile = 4096;      // elements per CTA
+
+struct AdamTensorDesc {
+  float* w;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* m_exp;
+  uint8_t* v_exp;
+  float* m_out;
+  float* v_out;
+  uint64_t n;
+  uint64_t tile_begin;   // first tile of this tensor in the plan
+  uint64_t block_begin;  // first block of this tensor in the plan (random bits)
+  float weight_decay;
+  float lr_scale;
+  uint32_t grad_bf16;
+  uint32_t reserved;
+};
+
+struct AdamLaunch {
+  const AdamTensorDesc* tensors;  // device
+  const uint32_t* tile_tensor;    // device: tensor of each tile
+  uint64_t total_tiles;
+  const float* grad_scale;        // device, or null
+  float alpha;                    // lr / (1 - beta1^step)
+  float lr;
+  float beta1, one_minus_beta1;
+  float beta2, one_minus_beta2;
+  float inv_sqrt_bc2;             // 1 / sqrt(1 - beta2^step)
+  float eps;
+  uint32_t key;                   // seed and step folded
+};
+
+uint32_t adam_key(uint64_t seed, uint64_t step);
+cudaError_t launch_adam32(const AdamLaunch& a, cudaStream_t stream);
+cudaError_t launch_adam8(const AdamLaunch& a, cudaStream_t stream);
+cudaError_t launch_adam_export(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
+                               uint64_t total_tiles, cudaStream_t stream);
+// partials: kNormMaxCtas doubles; ticket: one word, zero before and after.
+constexpr int kNormMaxCtas = 2048;
+cudaError_t launch_grad_norm(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
+                             uint64_t total_tiles, int sms, double* partials, uint32_t* ticket,
+                             float max_norm, float* norm_out, float* clip_out, cudaStream_t stream);
+
+// ---------------------------------------------------------------- logit shaping
+struct LogitsArgs {
+  uint64_t rows;
+  uint32_t vocab;
+  uint32_t slices;          // CTAs per row
+  uint32_t slice;           // elements per CTA
+  const int32_t* tokens;
+  int64_t ntokens;
+  const int64_t* begin;
+  const int64_t* split;
+  const int64_t* end;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const float* temperature;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  int64_t nbias;
+  const int64_t* bias_begin;
+  const uint32_t* mask;
+  int64_t mask_rows;
+  uint64_t mask_stride;
+  const int32_t* mask_row;
+  const void* src;          // logits (forward) or dout (backward)
+  uint64_t src_stride;
+  const void* raw;          // backward: raw logits
+  uint64_t raw_stride;
+  void* dst;
+  uint64_t dst_stride;
+  uint32_t* error_word;
+};
+cudaError_t launch_logits_shape(LogitsArgs a, int in_type, int out_type, int sms,
+                                cudaStream_t stream);
+cudaError_t launch_logits_backward(LogitsArgs a, int in_type, int out_type, int sms,
+                                   cudaStream_t stream);
+
 int sm_count(int device);
 
 }  // namespace pulse

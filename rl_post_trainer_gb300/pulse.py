@@ -144,6 +144,57 @@ class PulseLocoTensor(ctypes.Structure):
     ]
 
 
+class PulseAdamTensor(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_uint64),
+        ("master", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("grad_dtype", ctypes.c_int),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_exp", ctypes.c_void_p),
+        ("v_exp", ctypes.c_void_p),
+        ("m_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("weight_decay", ctypes.c_float),
+        ("lr_scale", ctypes.c_float),
+    ]
+
+
+class PulseAdamHyper(ctypes.Structure):
+    _fields_ = [
+        ("step", ctypes.c_uint64),
+        ("seed", ctypes.c_uint64),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+    ]
+
+
+class PulseLogitsShaping(ctypes.Structure):
+    _fields_ = [
+        ("vocab", ctypes.c_uint64),
+        ("tokens", ctypes.c_void_p),
+        ("ntokens", ctypes.c_uint64),
+        ("begin", ctypes.c_void_p),
+        ("split", ctypes.c_void_p),
+        ("end", ctypes.c_void_p),
+        ("repetition", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p),
+        ("bias_tokens", ctypes.c_void_p),
+        ("bias_values", ctypes.c_void_p),
+        ("nbias", ctypes.c_uint64),
+        ("bias_begin", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("mask_rows", ctypes.c_uint64),
+        ("mask_stride", ctypes.c_uint64),
+        ("mask_row", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -214,6 +265,15 @@ def lib():
             "pulse_nvfp4_quantize": ([P, U64, P, P, P, P], I),
             "pulse_nvfp4_encode": ([P, P, P, U64, P, P, P, P, P, P, P], I),
             "pulse_nvfp4_encode_multi": ([P, P, P, P], I),
+            "pulse_adam_plan_create": ([ctypes.POINTER(PulseAdamTensor), I, I, ctypes.POINTER(P)], I),
+            "pulse_adam_plan_destroy": ([P], I),
+            "pulse_adam_plan_set_grads": ([P, ctypes.POINTER(P), P], I),
+            "pulse_grad_norm_multi": ([P, ctypes.c_float, P, P, P], I),
+            "pulse_adam_step_multi": ([P, ctypes.POINTER(PulseAdamHyper), P, P], I),
+            "pulse_adam_export_multi": ([P, P], I),
+            "pulse_logits_shape": ([ctypes.POINTER(PulseLogitsShaping), U64, P, U64, I, P, U64, I, P], I),
+            "pulse_logits_shape_backward": ([ctypes.POINTER(PulseLogitsShaping), U64, P, U64, I,
+                                             P, U64, I, P, U64, P], I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -1145,3 +1205,314 @@ class PackJob:
             st = lib().pulse_unpack_indices_multi(self._unpack_arr, self.nsegs, _stream(self.device))
         _raise(st, "pulse_unpack_indices_multi")
         return self.unpacked
+
+
+# ------------------------------------------------------------ optimizer step
+
+ADAM_BLOCK = 256
+_F32_BF16 = (torch.float32, torch.bfloat16)
+
+
+def _type_code(t: torch.Tensor) -> int:
+    return 1 if t.dtype == torch.bfloat16 else 0
+
+
+class _on_device:
+    """``dev`` as the current CUDA device inside a with block; no CUDA call
+    where it already is."""
+
+    __slots__ = ("index", "back")
+
+    def __init__(self, dev: torch.device):
+        self.index, self.back = dev.index, None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.index is not None and now != self.index:
+            self.back = now
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def adam_blocks(n: int) -> int:
+    """Exponent bytes of one 8-bit moment of ``n`` elements."""
+    return (int(n) + ADAM_BLOCK - 1) // ADAM_BLOCK
+
+
+class AdamTensorSlot:
+    """Buffers of one model tensor for an AdamPlan.
+
+    ``grad`` is FP32 or BF16 and may be None (no gradient: the tensor is left
+    alone). FP32 moments: ``m`` and ``v`` are FP32. 8-bit moments: ``m`` and
+    ``v`` are uint8 codes, ``m_exp`` and ``v_exp`` hold ``adam_blocks(n)`` uint8
+    exponents, and ``m_out`` / ``v_out`` (FP32) receive ``export_states``.
+    All-zero state is a fresh state in both forms.
+    """
+
+    def __init__(self, n: int, master=None, grad=None, m=None, v=None, m_exp=None, v_exp=None,
+                 m_out=None, v_out=None, weight_decay: float = 0.0, lr_scale: float = 1.0,
+                 grad_dtype: Optional[torch.dtype] = None):
+        self.n = int(n)
+        self.master, self.grad, self.m, self.v = master, grad, m, v
+        self.m_exp, self.v_exp, self.m_out, self.v_out = m_exp, v_exp, m_out, v_out
+        self.weight_decay, self.lr_scale = float(weight_decay), float(lr_scale)
+        self.grad_dtype = grad_dtype if grad_dtype is not None else (
+            torch.float32 if grad is None else grad.dtype)
+        if self.grad_dtype not in _F32_BF16:
+            raise TypeError(f"grad_dtype: {self.grad_dtype} not in {_F32_BF16}")
+
+
+class AdamPlan:
+    """pulse_adam_plan: gradient norm and AdamW step of a whole model, one launch each.
+
+    ``state_bits`` is 32 (FP32 moments) or 8 (8-bit moments in blocks of 256).
+    """
+
+    def __init__(self, slots: Sequence[AdamTensorSlot], device: Optional[torch.device] = None,
+                 state_bits: int = 32):
+        if len(slots) == 0:
+            raise ValueError("a plan needs at least one tensor")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
+        self.slots = list(slots)
+        self.state_bits = state_bits
+        dev = device
+        moment = (torch.uint8,) if state_bits == 8 else (torch.float32,)
+        arr = (PulseAdamTensor * len(slots))()
+        for i, s in enumerate(slots):
+            for name, t, dtypes, numel in (
+                    ("master", s.master, (torch.float32,), s.n),
+                    ("grad", s.grad, (s.grad_dtype,), s.n),
+                    ("m", s.m, moment, s.n), ("v", s.v, moment, s.n),
+                    ("m_exp", s.m_exp, (torch.uint8,), adam_blocks(s.n)),
+                    ("v_exp", s.v_exp, (torch.uint8,), adam_blocks(s.n)),
+                    ("m_out", s.m_out, (torch.float32,), s.n),
+                    ("v_out", s.v_out, (torch.float32,), s.n)):
+                if t is None:
+                    continue
+                if dev is None:
+                    dev = t.device
+                _need(t, name, dtypes, dev, numel)
+            arr[i] = PulseAdamTensor(
+                s.n, _ptr(s.master), _ptr(s.grad), 1 if s.grad_dtype == torch.bfloat16 else 0,
+                _ptr(s.m), _ptr(s.v), _ptr(s.m_exp), _ptr(s.v_exp), _ptr(s.m_out), _ptr(s.v_out),
+                s.weight_decay, s.lr_scale)
+        if dev is None:
+            raise ValueError("a plan needs at least one device buffer")
+        self.device = dev
+        self.ntensors = len(slots)
+        handle = ctypes.c_void_p()
+        with torch.cuda.device(dev):
+            st = lib().pulse_adam_plan_create(arr, len(slots), state_bits, ctypes.byref(handle))
+        _raise(st, "pulse_adam_plan_create")
+        self._h = handle
+
+    def set_grads(self, grads: Sequence[Optional[torch.Tensor]]):
+        """New gradient tensors (None: no gradient), of the types and sizes the plan has."""
+        if len(grads) != self.ntensors:
+            raise ValueError(f"{len(grads)} gradients, the plan has {self.ntensors} tensors")
+        arr = (ctypes.c_void_p * self.ntensors)()
+        for i, (s, g) in enumerate(zip(self.slots, grads)):
+            if g is not None:
+                _need(g, "grad", (s.grad_dtype,), self.device, s.n)
+                arr[i] = g.data_ptr()
+        with _on_device(self.device):
+            st = lib().pulse_adam_plan_set_grads(self._h, arr, _stream(self.device))
+        _raise(st, "pulse_adam_plan_set_grads")
+        for s, g in zip(self.slots, grads):
+            s.grad = g
+
+    def grad_norm(self, max_norm: float = float("inf"), norm_out: Optional[torch.Tensor] = None,
+                  clip_out: Optional[torch.Tensor] = None):
+        """(norm, clip): one-element FP32 tensors on the device. ``clip`` is the
+        factor that brings the norm down to ``max_norm``, NaN for a norm that is
+        not finite; ``step(grad_scale=clip)`` applies it, and skips on NaN."""
+        both = torch.empty(2, dtype=torch.float32, device=self.device) \
+            if norm_out is None or clip_out is None else None
+        if norm_out is None:
+            norm_out = both[:1]
+        else:
+            _need(norm_out, "norm_out", (torch.float32,), self.device, min_numel=1)
+        if clip_out is None:
+            clip_out = both[1:]
+        else:
+            _need(clip_out, "clip_out", (torch.float32,), self.device, min_numel=1)
+        with _on_device(self.device):
+            st = lib().pulse_grad_norm_multi(self._h, max_norm, norm_out.data_ptr(),
+                                             clip_out.data_ptr(), _stream(self.device))
+        _raise(st, "pulse_grad_norm_multi")
+        return norm_out, clip_out
+
+    def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+             grad_scale: Optional[torch.Tensor] = None, seed: int = 0):
+        """One AdamW step in place (``step`` is 1 for the first). ``grad_scale``:
+        one FP32 value on the device that multiplies the gradients; ``seed``: of
+        the stochastic rounding of 8-bit moments."""
+        if step < 1:
+            raise ValueError(f"step: {step}, the first step is 1")
+        scale = 0
+        if grad_scale is not None:
+            _need(grad_scale, "grad_scale", (torch.float32,), self.device, min_numel=1)
+            scale = grad_scale.data_ptr()
+        h = PulseAdamHyper(step, seed & 0xFFFFFFFFFFFFFFFF, lr, beta1, beta2, eps)
+        with _on_device(self.device):
+            st = lib().pulse_adam_step_multi(self._h, ctypes.byref(h), scale, _stream(self.device))
+        _raise(st, "pulse_adam_step_multi")
+
+    def export_states(self):
+        """8-bit moments as FP32 values into every slot's ``m_out`` and ``v_out``."""
+        with _on_device(self.device):
+            st = lib().pulse_adam_export_multi(self._h, _stream(self.device))
+        _raise(st, "pulse_adam_export_multi")
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            with torch.cuda.device(self.device):
+                lib().pulse_adam_plan_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+# ------------------------------------------------------------- logit shaping
+
+class LogitsPlan:
+    """Settings of up to ``rows`` requests (or training positions) for pulse_logits_shape.
+
+    The tensors are bound once and read at every call, so a decode loop updates
+    them in place (appends to ``tokens``, moves ``end``) and calls ``shape``
+    again. Any of them may be None; the step it belongs to is left out.
+
+    * ``tokens`` int32, with ``begin``, ``split``, ``end`` int64 per row: the history
+      of row r is ``tokens[begin[r]:end[r]]``, generated from ``split[r]`` on
+    * ``repetition``, ``presence``, ``frequency``, ``temperature``: FP32 per row
+    * ``bias_tokens`` int32 and ``bias_values`` FP32 with ``bias_begin`` int64 (rows + 1)
+    * ``mask`` int32 ``[M, >= ceil(vocab / 32)]``: bit t & 31 of word t >> 5 allows token
+      t; ``mask_row`` int32 per row names its mask row, below 0 for none
+    """
+
+    def __init__(self, rows: int, vocab: int, device: Optional[torch.device] = None, *, tokens=None,
+                 begin=None, split=None, end=None, repetition=None, presence=None, frequency=None,
+                 temperature=None, bias_tokens=None, bias_values=None, bias_begin=None, mask=None,
+                 mask_row=None):
+        self.rows, self.vocab = int(rows), int(vocab)
+        if self.rows < 0 or not 1 <= self.vocab < 2 ** 31:
+            raise ValueError(f"rows {rows} or vocab {vocab} out of range")
+        if tokens is not None and (begin is None or end is None):
+            raise ValueError("tokens need begin and end")
+        if bias_tokens is not None and (bias_values is None or bias_begin is None):
+            raise ValueError("bias_tokens need bias_values and bias_begin")
+        dev = device
+        i32, i64, f32 = (torch.int32, torch.uint32), (torch.int64,), (torch.float32,)
+        nbias = 0 if bias_tokens is None else bias_tokens.numel()
+        self.tensors = dict(tokens=tokens, begin=begin, split=split, end=end, repetition=repetition,
+                            presence=presence, frequency=frequency, temperature=temperature,
+                            bias_tokens=bias_tokens, bias_values=bias_values, bias_begin=bias_begin,
+                            mask=mask, mask_row=mask_row)
+        for name, dtypes, room in (
+                ("tokens", i32, None), ("begin", i64, self.rows), ("split", i64, self.rows),
+                ("end", i64, self.rows), ("repetition", f32, self.rows), ("presence", f32, self.rows),
+                ("frequency", f32, self.rows), ("temperature", f32, self.rows),
+                ("bias_tokens", i32, None), ("bias_values", f32, nbias),
+                ("bias_begin", i64, self.rows + 1), ("mask_row", (torch.int32,), self.rows)):
+            t = self.tensors[name]
+            if t is None:
+                continue
+            if dev is None:
+                dev = t.device
+            _need(t, name, dtypes, dev, min_numel=room)
+        mask_rows = mask_stride = 0
+        if mask is not None:
+            if dev is None:
+                dev = mask.device
+            if not mask.is_cuda or mask.dtype not in i32:
+                raise TypeError("mask: expected an int32 CUDA tensor")
+            words = (self.vocab + 31) // 32
+            if mask.dim() != 2 or mask.shape[1] < words or mask.stride(1) != 1:
+                raise ValueError(f"mask: expected [M, >= {words}] with contiguous rows, got {tuple(mask.shape)}")
+            if mask.device != dev:
+                raise ValueError(f"mask: on {mask.device}, expected {dev}")
+            if mask.shape[0] > 1 and mask.stride(0) < words:
+                raise ValueError(f"mask: rows {mask.stride(0)} words apart, need at least {words}")
+            mask_rows, mask_stride = mask.shape[0], max(mask.stride(0), words)
+            if mask_row is None and mask_rows < self.rows:
+                raise ValueError(f"mask: {mask_rows} rows, need at least {self.rows} without mask_row")
+        self.device = dev
+        p = {k: 0 if t is None else t.data_ptr() for k, t in self.tensors.items()}
+        self._c = PulseLogitsShaping(
+            self.vocab, p["tokens"], 0 if tokens is None else tokens.numel(), p["begin"], p["split"],
+            p["end"], p["repetition"], p["presence"], p["frequency"], p["temperature"],
+            p["bias_tokens"], p["bias_values"], nbias, p["bias_begin"], p["mask"], mask_rows,
+            mask_stride, p["mask_row"])
+        self._ref = ctypes.byref(self._c)
+
+    def _rows_of(self, t: torch.Tensor, name: str, dtypes, like: Optional[torch.Tensor] = None):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}: expected a CUDA tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        if t.dim() != 2 or t.shape[1] != self.vocab or t.shape[0] > self.rows:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [<= {self.rows}, {self.vocab}]")
+        if t.stride(1) != 1 and self.vocab > 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        if like is not None and t.shape[0] != like.shape[0]:
+            raise ValueError(f"{name}: {t.shape[0]} rows, expected {like.shape[0]}")
+        if self.device is None:
+            self.device = t.device
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), self.vocab)
+
+    def shape(self, logits: torch.Tensor, out: Optional[torch.Tensor] = None,
+              out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        """Shaped logits of the first ``logits.shape[0]`` rows. ``out`` may be
+        ``logits`` (in place); by default a new tensor of ``out_dtype`` (that of
+        ``logits``). FP32 logits give FP32, BF16 logits BF16 or FP32."""
+        src, stride = self._rows_of(logits, "logits", _F32_BF16)
+        if out is None:
+            out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
+        allowed = _F32_BF16 if logits.dtype == torch.bfloat16 else (torch.float32,)
+        dst, out_stride = self._rows_of(out, "out", allowed, logits)
+        with _on_device(self.device):
+            st = lib().pulse_logits_shape(self._ref, logits.shape[0], src, stride, _type_code(logits),
+                                          dst, out_stride, _type_code(out), _stream(self.device))
+        _raise(st, "pulse_logits_shape")
+        return out
+
+    def backward(self, dout: torch.Tensor, logits: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient with respect to the raw ``logits`` (needed where the plan has
+        a repetition penalty and a history; not the shaped ones), given that with
+        respect to the shaped ones. ``out`` (of the raw logits' type, by default
+        new) may be ``dout``."""
+        d, d_stride = self._rows_of(dout, "dout", _F32_BF16)
+        if logits is None and self._c.tokens and self._c.repetition:
+            raise ValueError("logits: the gradient of the repetition penalty needs the raw logits")
+        raw, raw_stride = 0, 0
+        if logits is not None:
+            raw, raw_stride = self._rows_of(logits, "logits", _F32_BF16, dout)
+        in_dtype = logits.dtype if logits is not None else (dout if out is None else out).dtype
+        if in_dtype == torch.float32 and dout.dtype != torch.float32:
+            raise TypeError("dout: FP32 logits have FP32 shaped logits")
+        if out is None:
+            out = torch.empty(dout.shape, dtype=in_dtype, device=dout.device)
+        dst, out_stride = self._rows_of(out, "out", (in_dtype,), dout)
+        with _on_device(self.device):
+            st = lib().pulse_logits_shape_backward(
+                self._ref, dout.shape[0], d, d_stride, _type_code(dout), raw, raw_stride,
+                1 if in_dtype == torch.bfloat16 else 0, dst, out_stride, _stream(self.device))
+        _raise(st, "pulse_logits_shape_backward")
+        return out
