@@ -348,9 +348,11 @@ cudaError_t launch_xor_apply(const TensorDesc& one, const TensorDesc* tensors,
 // ---------------------------------------------------------------- AdamW step
 constexpr int kAdamBlock = 256;      // elements sharing an exponent byte (8-bit moments)
 constexpr int kAdamThreads = 256;
-constexpr int kAdamTile = 4096;      // elements per CTA
+constexpr uint32_t kAdam32Tile = 2048;  // elements per CTA, FP32 moments
+constexpr uint32_t kAdam8Tile = 8192;       // 8-bit moments
+constexpr uint32_t kAdam8TileSmall = 2048;  // 8-bit moments, small plans
 
-struct AdamTensorDesc {
+struct alignas(16) AdamTensorDesc {  // read in 16-byte pieces
   float* w;
   const void* g;
   void* m;
@@ -365,13 +367,19 @@ struct AdamTensorDesc {
   float weight_decay;
   float lr_scale;
   uint32_t grad_bf16;
-  uint32_t reserved;
+  // Elements before the first one from which every buffer can be accessed in
+  // groups of 8 (32 bytes of FP32, 16 of BF16, 8 codes); kAdamNoGroups where no
+  // common one exists. 8-bit moments: 0 or kAdamNoGroups, since a group must
+  // not straddle two blocks.
+  uint32_t lead;
 };
+constexpr uint32_t kAdamNoGroups = 8;
 
 struct AdamLaunch {
   const AdamTensorDesc* tensors;  // device
   const uint32_t* tile_tensor;    // device: tensor of each tile
   uint64_t total_tiles;
+  uint32_t tile;                  // elements per tile
   const float* grad_scale;        // device, or null
   float alpha;                    // lr / (1 - beta1^step)
   float lr;
@@ -379,6 +387,7 @@ struct AdamLaunch {
   float beta2, one_minus_beta2;
   float inv_sqrt_bc2;             // 1 / sqrt(1 - beta2^step)
   float eps;
+  float one;                      // 1.0f (see add2 in adam.cu)
   uint32_t key;                   // seed and step folded
 };
 
@@ -386,11 +395,11 @@ uint32_t adam_key(uint64_t seed, uint64_t step);
 cudaError_t launch_adam32(const AdamLaunch& a, cudaStream_t stream);
 cudaError_t launch_adam8(const AdamLaunch& a, cudaStream_t stream);
 cudaError_t launch_adam_export(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
-                               uint64_t total_tiles, cudaStream_t stream);
-// partials: kNormMaxCtas doubles; ticket: one word, zero before and after.
+                               uint32_t tile, uint64_t total_tiles, cudaStream_t stream);
+// partials: kNormMaxCtas words; ticket: one word, zero before and after.
 constexpr int kNormMaxCtas = 2048;
 cudaError_t launch_grad_norm(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
-                             uint64_t total_tiles, int sms, double* partials, uint32_t* ticket,
+                             uint32_t tile, uint64_t total_tiles, int sms, uint64_t* partials, uint32_t* ticket,
                              float max_norm, float* norm_out, float* clip_out, cudaStream_t stream);
 
 // ---------------------------------------------------------------- logit shaping

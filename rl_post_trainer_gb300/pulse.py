@@ -1228,13 +1228,24 @@ class _on_device:
 
     def __enter__(self):
         now = torch.cuda.current_device()
-        if self.index is not None and now != self.index:
+        if now != self.index:
             self.back = now
             torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
         if self.back is not None:
             torch.cuda.set_device(self.back)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    """torch's current stream of ``dev`` as a number, without building a Stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _indexed(dev: torch.device) -> torch.device:
+    """``dev`` with its index (torch.device("cuda") has none)."""
+    dev = torch.device(dev)
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 def adam_blocks(n: int) -> int:
@@ -1279,7 +1290,7 @@ class AdamPlan:
             raise ValueError(f"state_bits: {state_bits}, expected 8 or 32")
         self.slots = list(slots)
         self.state_bits = state_bits
-        dev = device
+        dev = None if device is None else _indexed(device)
         moment = (torch.uint8,) if state_bits == 8 else (torch.float32,)
         arr = (PulseAdamTensor * len(slots))()
         for i, s in enumerate(slots):
@@ -1320,7 +1331,7 @@ class AdamPlan:
                 _need(g, "grad", (s.grad_dtype,), self.device, s.n)
                 arr[i] = g.data_ptr()
         with _on_device(self.device):
-            st = lib().pulse_adam_plan_set_grads(self._h, arr, _stream(self.device))
+            st = lib().pulse_adam_plan_set_grads(self._h, arr, _raw_stream(self.device))
         _raise(st, "pulse_adam_plan_set_grads")
         for s, g in zip(self.slots, grads):
             s.grad = g
@@ -1330,19 +1341,17 @@ class AdamPlan:
         """(norm, clip): one-element FP32 tensors on the device. ``clip`` is the
         factor that brings the norm down to ``max_norm``, NaN for a norm that is
         not finite; ``step(grad_scale=clip)`` applies it, and skips on NaN."""
-        both = torch.empty(2, dtype=torch.float32, device=self.device) \
-            if norm_out is None or clip_out is None else None
         if norm_out is None:
-            norm_out = both[:1]
+            norm_out = torch.empty(1, dtype=torch.float32, device=self.device)
         else:
             _need(norm_out, "norm_out", (torch.float32,), self.device, min_numel=1)
         if clip_out is None:
-            clip_out = both[1:]
+            clip_out = torch.empty(1, dtype=torch.float32, device=self.device)
         else:
             _need(clip_out, "clip_out", (torch.float32,), self.device, min_numel=1)
         with _on_device(self.device):
             st = lib().pulse_grad_norm_multi(self._h, max_norm, norm_out.data_ptr(),
-                                             clip_out.data_ptr(), _stream(self.device))
+                                             clip_out.data_ptr(), _raw_stream(self.device))
         _raise(st, "pulse_grad_norm_multi")
         return norm_out, clip_out
 
@@ -1359,13 +1368,13 @@ class AdamPlan:
             scale = grad_scale.data_ptr()
         h = PulseAdamHyper(step, seed & 0xFFFFFFFFFFFFFFFF, lr, beta1, beta2, eps)
         with _on_device(self.device):
-            st = lib().pulse_adam_step_multi(self._h, ctypes.byref(h), scale, _stream(self.device))
+            st = lib().pulse_adam_step_multi(self._h, ctypes.byref(h), scale, _raw_stream(self.device))
         _raise(st, "pulse_adam_step_multi")
 
     def export_states(self):
         """8-bit moments as FP32 values into every slot's ``m_out`` and ``v_out``."""
         with _on_device(self.device):
-            st = lib().pulse_adam_export_multi(self._h, _stream(self.device))
+            st = lib().pulse_adam_export_multi(self._h, _raw_stream(self.device))
         _raise(st, "pulse_adam_export_multi")
 
     def close(self):
@@ -1415,7 +1424,7 @@ class LogitsPlan:
             raise ValueError("tokens need begin and end")
         if bias_tokens is not None and (bias_values is None or bias_begin is None):
             raise ValueError("bias_tokens need bias_values and bias_begin")
-        dev = device
+        dev = None if device is None else _indexed(device)
         i32, i64, f32 = (torch.int32, torch.uint32), (torch.int64,), (torch.float32,)
         nbias = 0 if bias_tokens is None else bias_tokens.numel()
         self.tensors = dict(tokens=tokens, begin=begin, split=split, end=end, repetition=repetition,
@@ -1488,7 +1497,7 @@ class LogitsPlan:
         dst, out_stride = self._rows_of(out, "out", allowed, logits)
         with _on_device(self.device):
             st = lib().pulse_logits_shape(self._ref, logits.shape[0], src, stride, _type_code(logits),
-                                          dst, out_stride, _type_code(out), _stream(self.device))
+                                          dst, out_stride, _type_code(out), _raw_stream(self.device))
         _raise(st, "pulse_logits_shape")
         return out
 
@@ -1513,6 +1522,6 @@ class LogitsPlan:
         with _on_device(self.device):
             st = lib().pulse_logits_shape_backward(
                 self._ref, dout.shape[0], d, d_stride, _type_code(dout), raw, raw_stride,
-                1 if in_dtype == torch.bfloat16 else 0, dst, out_stride, _stream(self.device))
+                1 if in_dtype == torch.bfloat16 else 0, dst, out_stride, _raw_stream(self.device))
         _raise(st, "pulse_logits_shape_backward")
         return out
