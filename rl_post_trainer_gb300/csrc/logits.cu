@@ -2,11 +2,10 @@
 // biases, temperature, grammar masks) and its gradient, with the formulas of
 // include/pulse.h.
 //
-// One CTA takes a slice of a row's vocabulary. It reads the row's history and
-// bias list once, keeps in shared memory what falls into its slice (a bit per
-// token, the count of generated ones, the last bias entry), computes the few
-// touched values with full warps, and then streams over the slice: scale, mask,
-// and where a token's bit is set the value from shared memory.
+// A row is cut into slices, one CTA each. A CTA asks for its slice, reads the
+// row's history and bias list meanwhile, keeps a bit for every token of its slice
+// that they name (and, where tokens are counted or biased, a word), and then works
+// off the slice from registers.
 #include "pulse.h"
 #include "pulse_device.cuh"
 #include "pulse_internal.h"
@@ -14,21 +13,24 @@
 namespace pulse {
 namespace {
 
+#ifndef PULSE_LOGITS_MIN
+#define PULSE_LOGITS_MIN 4
+#endif
+#ifndef PULSE_LOGITS_GROUPS
+#define PULSE_LOGITS_GROUPS 4
+#endif
 #ifndef PULSE_LOGITS_THREADS
 #define PULSE_LOGITS_THREADS 256
 #endif
-#ifndef PULSE_LOGITS_SLICE
-#define PULSE_LOGITS_SLICE 8192
-#endif
-#ifndef PULSE_LOGITS_SLICE_BACK
-#define PULSE_LOGITS_SLICE_BACK 8192
-#endif
-#ifndef PULSE_LOGITS_BATCH
-#define PULSE_LOGITS_BATCH 2
-#endif
 constexpr int kThreads = PULSE_LOGITS_THREADS;
+constexpr int kMinCtas = PULSE_LOGITS_MIN;
+// Groups of 8 elements a thread holds: its whole part of a slice, asked for
+// before the history is read.
+constexpr int kGroups = PULSE_LOGITS_GROUPS;
 constexpr uint32_t kSliceMin = 2048;
-constexpr int kBatch = PULSE_LOGITS_BATCH;  // groups of 8 elements a thread has in flight
+constexpr uint32_t kSliceMax = 8u * kThreads * kGroups - 32u;
+constexpr uint32_t kWords = (kSliceMax + 8u + 31u) / 32u;  // of a bitmap of a slice's places
+constexpr uint32_t kPlaces = kWords * 32u;
 
 // A group is 8 elements of a row, 16 bytes of BF16 or 32 of FP32.
 __device__ __forceinline__ float load_elem(const float* p) { return *p; }
@@ -39,20 +41,31 @@ __device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_elem(uint16_t* p, float x) {
   *p = uint16_t(cvt_bf16x2_rn(x, 0.0f));
 }
-__device__ __forceinline__ void load_group(const float* p, float (&x)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+// A group as it lies in memory.
+template <typename T>
+struct Raw {
+  uint32_t u[2 * sizeof(T)];
+};
+__device__ __forceinline__ void load_group(const float* p, Raw<float>& x) {
+  asm volatile("ld.global.L1::no_allocate.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(x.u[0]), "=r"(x.u[1]), "=r"(x.u[2]), "=r"(x.u[3]), "=r"(x.u[4]), "=r"(x.u[5]),
+                 "=r"(x.u[6]), "=r"(x.u[7])
                : "l"(p));
 }
-__device__ __forceinline__ void load_group(const uint16_t* p, float (&x)[8]) {
-  uint32_t u[4];
+__device__ __forceinline__ void load_group(const uint16_t* p, Raw<uint16_t>& x) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+               : "=r"(x.u[0]), "=r"(x.u[1]), "=r"(x.u[2]), "=r"(x.u[3])
                : "l"(p));
+}
+__device__ __forceinline__ void values(const Raw<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(r.u[k]);
+}
+__device__ __forceinline__ void values(const Raw<uint16_t>& r, float (&x)[8]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(u[k] << 16);
-    x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    x[2 * k] = __uint_as_float(r.u[k] << 16);
+    x[2 * k + 1] = __uint_as_float(r.u[k] & 0xFFFF0000u);
   }
 }
 __device__ __forceinline__ void store_group(float* p, const float (&x)[8]) {
@@ -70,44 +83,24 @@ __device__ __forceinline__ uint32_t lead_of(const T* p) {
   return uint32_t(0u - uint32_t(reinterpret_cast<uintptr_t>(p) / sizeof(T))) & 7u;
 }
 
-// A temperature that is not above 0 (greedy decoding) leaves the row as it is.
-__device__ __forceinline__ float inverse_temperature(const float* t, uint64_t row) {
-  if (t == nullptr) return 1.0f;
-  const float x = t[row];
-  return x > 0.0f ? __fdiv_rn(1.0f, x) : 1.0f;
-}
-
 struct Range {
   int64_t begin, split, end;
 };
 
 // The row's history, empty (and recorded) where its offsets do not fit.
 __device__ __forceinline__ Range history_of(const LogitsArgs& a, uint64_t row) {
-  Range r{0, 0, 0};
-  if (a.tokens == nullptr) return r;
   const int64_t b = a.begin[row], e = a.end[row];
   const int64_t s = a.split ? a.split[row] : b;
-  if (b < 0 || e < b || e > a.ntokens || s < b || s > e) {
-    if (threadIdx.x == 0) record_error(a.error_word, kErrIndex);
-    return r;
-  }
-  r.begin = b;
-  r.split = s;
-  r.end = e;
-  return r;
+  if (b >= 0 && s >= b && e >= s && e <= a.ntokens) return {b, s, e};
+  record_error(a.error_word, kErrIndex);
+  return {0, 0, 0};
 }
 
 __device__ __forceinline__ Range bias_of(const LogitsArgs& a, uint64_t row) {
-  Range r{0, 0, 0};
-  if (a.bias_tokens == nullptr) return r;
   const int64_t b = a.bias_begin[row], e = a.bias_begin[row + 1];
-  if (b < 0 || e < b || e > a.nbias) {
-    if (threadIdx.x == 0) record_error(a.error_word, kErrIndex);
-    return r;
-  }
-  r.begin = r.split = b;
-  r.end = e;
-  return r;
+  if (b >= 0 && e >= b && e <= a.nbias) return {b, b, e};
+  record_error(a.error_word, kErrIndex);
+  return {0, 0, 0};
 }
 
 // The row's mask words, or null.
@@ -130,277 +123,406 @@ __device__ __forceinline__ uint32_t mask_bits8(const uint32_t* mask, uint32_t t)
 }
 
 // This CTA's part of a row: tokens [first, stop), groups from `base` on. Token t
-// has place t - base + 8 in the shared tables, so that a group's bits are a byte
-// of the bitmap and the tokens before the first group (row start) have places
-// below 8.
+// has place t - base + 8, so that a group's bits are a byte of the bitmap and the
+// tokens in front of the first group (row start) have places below 8.
 struct Slice {
-  uint64_t row;
+  uint32_t row;
   uint32_t first, base, stop;
-  bool grouped;  // source and destination rows share their group boundaries
+  bool grouped;  // all rows involved share their group boundaries
 };
 
 template <typename TSrc, typename TDst>
 __device__ __forceinline__ Slice slice_of(const LogitsArgs& a, const TSrc*& src, TDst*& dst) {
   Slice s;
   s.row = blockIdx.x / a.slices;
-  const uint32_t k = uint32_t(blockIdx.x % a.slices);
+  const uint32_t k = blockIdx.x % a.slices;
   src += s.row * a.src_stride;
   dst += s.row * a.dst_stride;
-  const uint32_t lead = lead_of(src);
+  uint32_t lead = lead_of(src);
   s.grouped = lead == lead_of(dst);
-  s.base = (s.grouped ? lead : 0u) + k * a.slice;
+  if (!s.grouped) lead = 0u;
+  s.base = lead + k * a.slice;
   s.first = k == 0 ? 0u : min(s.base, a.vocab);
   s.stop = k + 1 == a.slices ? a.vocab : min(s.base + a.slice, a.vocab);
   return s;
 }
 
-// Calls f(token, position) for the entries [begin, end) of a list of tokens,
-// spread over the CTA, four at a time where the list is aligned for it.
+// Calls f(in, place, position) for the entries [begin, end) of a list of tokens,
+// a warp's lanes together; `in`: the entry belongs to the slice. Calls in which no
+// lane has one are left out: with a dozen slices a row that is most of them. Tokens
+// outside the vocabulary are recorded.
 template <typename F>
-__device__ __forceinline__ void scan_tokens(const int32_t* tokens, int64_t begin, int64_t end, F f) {
-  const int64_t n = end - begin;
+__device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s, const int32_t* tokens,
+                                            int64_t begin, int64_t end, F f) {
   const int32_t* p = tokens + begin;
-  const int64_t lead = min(n, int64_t((0u - uint32_t(reinterpret_cast<uintptr_t>(p) / 4u)) & 3u));
-  const int64_t quads = (n - lead) / 4;
-#pragma unroll 2
-  for (int64_t q = threadIdx.x; q < quads; q += kThreads) {
-    const int4 t = __ldg(reinterpret_cast<const int4*>(p + lead) + q);
-    const int64_t i = begin + lead + 4 * q;
-    f(uint32_t(t.x), i);
-    f(uint32_t(t.y), i + 1);
-    f(uint32_t(t.z), i + 2);
-    f(uint32_t(t.w), i + 3);
-  }
-  if (threadIdx.x < lead) f(uint32_t(p[threadIdx.x]), begin + threadIdx.x);
-  const int64_t rest = lead + 4 * quads + threadIdx.x;
-  if (rest < n) f(uint32_t(p[rest]), begin + rest);
-}
-
-// Shared tables of a slice of S tokens (S + 8 places, rounded up).
-__host__ __device__ constexpr uint32_t places(uint32_t slice) { return (slice + 8u + 31u) & ~31u; }
-
-// Marks place u and appends it to the list of touched places if it is new.
-__device__ __forceinline__ void touch(uint32_t* bits, uint16_t* list, uint32_t* count, uint32_t u) {
-  const uint32_t bit = 1u << (u & 31u);
-  if (!(atomicOr(bits + (u >> 5), bit) & bit)) list[atomicAdd(count, 1u)] = uint16_t(u);
-}
-
-// Streams a slice: x -> override(x, place) where the place's bit is set, else
-// plain(x); masked tokens become `masked` without being read.
-template <typename TSrc, typename TDst, typename Plain, typename Override>
-__device__ __forceinline__ void stream_slice(const Slice& s, const TSrc* src, TDst* dst,
-                                             const uint32_t* mask, const uint32_t* bits,
-                                             float masked, Plain plain, Override over) {
-  const uint8_t* bytes = reinterpret_cast<const uint8_t*>(bits);
-  auto one = [&](uint32_t t) {
-    const uint32_t u = t - s.base + 8u;
-    float y = masked;
-    if (mask == nullptr || (mask[t >> 5] >> (t & 31u)) & 1u) {
-      const float x = load_elem(src + t);
-      y = bits && (bits[u >> 5] >> (u & 31u)) & 1u ? over(x, u) : plain(x);
-    }
-    store_elem(dst + t, y);
+  const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
+  const uint32_t vocab = a.vocab;
+  uint32_t bad = 0u;
+  auto one = [&](uint32_t t, int64_t i) {
+    const bool in = t - s.first < len;
+    bad |= t >= vocab;
+    if (__any_sync(0xFFFFFFFFu, in)) f(in, t - s.first + off, i);
   };
+  const int64_t n = end - begin;
+  const int64_t lead = min(n, int64_t((0u - uint32_t(reinterpret_cast<uintptr_t>(p) / 4u)) & 3u));
+  const int64_t quads = (n - lead) / 4, rest = lead + 4 * quads;
+  const int4* quad = reinterpret_cast<const int4*>(p + lead);
+  for (int64_t q = threadIdx.x & ~31u; q < quads; q += kThreads) {
+    const int64_t at = q + (threadIdx.x & 31u);
+    int4 t = make_int4(-1, -1, -1, -1);
+    const bool have = at < quads;
+    if (have) t = __ldg(quad + at);
+    const int64_t i = begin + lead + 4 * at;
+    const uint32_t before = bad;
+    one(uint32_t(t.x), i);
+    one(uint32_t(t.y), i + 1);
+    one(uint32_t(t.z), i + 2);
+    one(uint32_t(t.w), i + 3);
+    if (!have) bad = before;
+  }
+  // up to 3 entries in front of the aligned ones and 3 behind, by the first warp
+  if (threadIdx.x < 32u) {
+    const int64_t i = threadIdx.x < lead ? threadIdx.x : rest + (threadIdx.x - lead);
+    const bool have = i < n;
+    const uint32_t before = bad;
+    one(have ? uint32_t(p[i]) : 0xFFFFFFFFu, begin + i);
+    if (!have) bad = before;
+  }
+  if (bad) record_error(a.error_word, kErrIndex);
+}
+
+// This thread's groups of a slice. Masked tokens are not read where a whole group
+// is masked.
+template <typename TSrc>
+struct Groups {
+  Raw<TSrc> x[kGroups];
+  uint32_t ok[kGroups];  // a bit a token: open (0 past the slice)
+  uint32_t count;        // of the slice
+
+  __device__ __forceinline__ void load(const Slice& s, const TSrc* src, const uint32_t* mask) {
+    count = s.grouped && s.stop > s.base ? (s.stop - s.base) / 8u : 0u;
+#pragma unroll
+    for (int r = 0; r < kGroups; ++r) {
+      const uint32_t q = threadIdx.x + r * kThreads;
+      ok[r] = q >= count ? 0u : mask ? mask_bits8(mask, s.base + 8u * q) : 0xFFu;
+    }
+#pragma unroll
+    for (int r = 0; r < kGroups; ++r)
+      if (ok[r]) load_group(src + s.base + 8u * (threadIdx.x + r * kThreads), x[r]);
+  }
+};
+
+template <typename TDst>
+__device__ __forceinline__ void store_masked(TDst* p, float (&y)[8], uint32_t ok, float masked) {
+  if (ok != 0xFFu) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!((ok >> k) & 1u)) y[k] = masked;
+  }
+  store_group(p, y);
+}
+
+// Calls f(t) for the tokens outside the groups: all of them where there are no
+// groups, else the row's first few and last few.
+template <typename F>
+__device__ __forceinline__ void each_single(const Slice& s, uint32_t groups, F f) {
   if (!s.grouped) {
-    for (uint32_t t = s.first + threadIdx.x; t < s.stop; t += kThreads) one(t);
+    for (uint32_t t = s.first + threadIdx.x; t < s.stop; t += kThreads) f(t);
     return;
   }
-  const uint32_t groups = s.stop > s.base ? (s.stop - s.base) / 8u : 0u;
-  for (uint32_t g = threadIdx.x; g < groups; g += kBatch * kThreads) {
-    float x[kBatch][8];
-    uint32_t ok[kBatch];
-#pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
-      const uint32_t q = g + r * kThreads;
-      ok[r] = q >= groups ? 0u : mask ? mask_bits8(mask, s.base + 8u * q) : 0xFFu;
-    }
-#pragma unroll
-    for (int r = 0; r < kBatch; ++r)
-      if (ok[r]) load_group(src + s.base + 8u * (g + r * kThreads), x[r]);
-#pragma unroll
-    for (int r = 0; r < kBatch; ++r) {
-      const uint32_t q = g + r * kThreads;
-      if (q >= groups) break;
-      const uint32_t hit = bits ? bytes[q + 1u] & ok[r] : 0u;
-      float y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = plain(x[r][k]);
-      if (hit) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if ((hit >> k) & 1u) y[k] = over(x[r][k], 8u * q + 8u + k);
-      }
-      if (ok[r] != 0xFFu) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (!((ok[r] >> k) & 1u)) y[k] = masked;
-      }
-      store_group(dst + s.base + 8u * q, y);
-    }
-  }
-  // the row's first tokens and its last, outside the groups
   const uint32_t head = s.first < s.base ? min(s.base, s.stop) - s.first : 0u;
-  if (threadIdx.x < head) one(s.first + threadIdx.x);
+  if (threadIdx.x < head) f(s.first + threadIdx.x);
   const uint32_t tail = s.base + 8u * groups + threadIdx.x;
-  if (s.stop > s.base && tail < s.stop) one(tail);
+  if (s.stop > s.base && tail < s.stop) f(tail);
 }
 
+__device__ __forceinline__ bool open_token(const uint32_t* mask, uint32_t t) {
+  return mask == nullptr || ((mask[t >> 5] >> (t & 31u)) & 1u);
+}
+
+constexpr float kClosed = -__builtin_huge_valf();
+
+// What thread 0 reads of the row for all.
+struct RowSettings {
+  Range history, bias;
+  float rep, inv_rep, pres, freq, inv_t;
+};
+
+__device__ __forceinline__ void read_row(const LogitsArgs& a, uint32_t row, bool history, RowSettings& r) {
+  r.history = history ? history_of(a, row) : Range{0, 0, 0};
+  r.bias = a.bias_tokens ? bias_of(a, row) : Range{0, 0, 0};
+  r.rep = a.repetition ? a.repetition[row] : 1.0f;
+  r.inv_rep = __frcp_rn(r.rep);
+  r.pres = a.presence ? a.presence[row] : 0.0f;
+  r.freq = a.frequency ? a.frequency[row] : 0.0f;
+  const float t = a.temperature ? a.temperature[row] : 1.0f;
+  r.inv_t = t > 0.0f ? __frcp_rn(t) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
+}
+
+// Repetition penalty and temperature alone: a bit a token is all there is to keep.
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads) shape_kernel(const __grid_constant__ LogitsArgs a) {
-  extern __shared__ uint4 smem[];
-  __shared__ uint32_t touched;
-  const uint32_t n = places(a.slice);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem);         // a bit per place
-  uint32_t* state = bits + n / 32u;                           // history, then the value as float bits
-  uint16_t* list = reinterpret_cast<uint16_t*>(state + n);    // touched places
-  uint32_t* entry = reinterpret_cast<uint32_t*>(list + n);    // 1 + place in the bias list (bias only)
+__global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_constant__ LogitsArgs a) {
+  __shared__ uint32_t bits[kWords];
+  __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
   const Slice s = slice_of(a, src, dst);
-  const Range h = a.repetition || a.presence || a.frequency ? history_of(a, s.row) : Range{0, 0, 0};
-  const Range bl = bias_of(a, s.row);
   const uint32_t* mask = mask_of(a, s.row);
-  const float inv_t = inverse_temperature(a.temperature, s.row);
-  const bool any = h.end > h.begin || bl.end > bl.begin;
-  if (any) {
-    const bool bias = bl.end > bl.begin;
-    if (threadIdx.x == 0) touched = 0u;
-    for (uint32_t i = threadIdx.x; i < n / 32u; i += kThreads) bits[i] = 0u;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) state[i] = 0u;
-    if (bias)
-      for (uint32_t i = threadIdx.x; i < n; i += kThreads) entry[i] = 0u;
+  Groups<TIn> g;
+  g.load(s, src, mask);
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  if (threadIdx.x == 0) read_row(a, s.row, a.tokens && a.repetition, row);
+  __syncthreads();
+  if (row.history.end > row.history.begin) {
+    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t) {
+      if (in) atomicOr(bits + (u >> 5), 1u << (u & 31u));
+    });
     __syncthreads();
-    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
-    // state: bit 31 for a token of the prompt, below it the times generated
-    scan_tokens(a.tokens, h.begin, h.end, [&](uint32_t t, int64_t i) {
-      if (t - s.first < len) {
-        const uint32_t u = t - s.first + off;
-        if (i >= h.split)
-          atomicAdd(state + u, 1u);
-        else
-          atomicOr(state + u, 0x80000000u);
-        touch(bits, list, &touched, u);
-      } else if (t >= a.vocab) {
-        record_error(a.error_word, kErrIndex);
+  }
+  const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
+  auto seen = [&](float x) { return __fmul_rn(__fmul_rn(x, x > 0.0f ? inv_rep : rep), inv_t); };
+#pragma unroll
+  for (int r = 0; r < kGroups; ++r) {
+    const uint32_t q = threadIdx.x + r * kThreads;
+    if (q < g.count) {
+      const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
+      float x[8], y[8];
+      values(g.x[r], x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(x[k], inv_t);
+      if (hit) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = (hit >> k) & 1u ? seen(x[k]) : y[k];
+      }
+      store_masked(dst + s.base + 8u * q, y, g.ok[r], kClosed);
+    }
+  }
+  each_single(s, g.count, [&](uint32_t t) {
+    const uint32_t u = t - s.base + 8u;
+    float y = kClosed;
+    if (open_token(mask, t)) {
+      const float x = load_elem(src + t);
+      y = (bits[u >> 5] >> (u & 31u)) & 1u ? seen(x) : __fmul_rn(x, inv_t);
+    }
+    store_elem(dst + t, y);
+  });
+}
+
+// Everything: tokens are counted and biased.
+template <typename TIn, typename TOut>
+__global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_constant__ LogitsArgs a) {
+  extern __shared__ uint4 smem[];
+  // a word a place: bit 31 for a token of the prompt, below it the times it was
+  // generated; then the logit as the penalties and the bias leave it
+  uint32_t* word = reinterpret_cast<uint32_t*>(smem);
+  uint16_t* list = reinterpret_cast<uint16_t*>(word + kPlaces);  // places of the history, each once
+  __shared__ uint32_t bits[kWords];                              // places whose word is a logit
+  __shared__ uint32_t listed;
+  __shared__ RowSettings row;
+  const TIn* src = static_cast<const TIn*>(a.src);
+  TOut* dst = static_cast<TOut*>(a.dst);
+  const Slice s = slice_of(a, src, dst);
+  const uint32_t* mask = mask_of(a, s.row);
+  Groups<TIn> g;
+  g.load(s, src, mask);
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
+    reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (threadIdx.x == 0) {
+    listed = 0u;
+    read_row(a, s.row, a.tokens && (a.repetition || a.presence || a.frequency), row);
+  }
+  __syncthreads();
+  const uint32_t lane = threadIdx.x & 31u;
+  if (row.history.end > row.history.begin) {
+    const int64_t split = row.history.split;
+    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t i) {
+      uint32_t old = 1u;
+      if (in) old = i >= split ? atomicAdd(word + u, 1u) : atomicOr(word + u, 0x80000000u);
+      const uint32_t fresh = __ballot_sync(0xFFFFFFFFu, old == 0u);
+      if (fresh) {
+        uint32_t at = 0u;
+        if (lane == 0) at = atomicAdd(&listed, uint32_t(__popc(fresh)));
+        at = __shfl_sync(0xFFFFFFFFu, at, 0);
+        if (old == 0u) list[at + __popc(fresh & lanemask_lt())] = uint16_t(u);
       }
     });
-    if (bias)
-      scan_tokens(a.bias_tokens, bl.begin, bl.end, [&](uint32_t t, int64_t i) {
-        if (t - s.first < len) {
-          const uint32_t u = t - s.first + off;
-          atomicMax(entry + u, uint32_t(i - bl.begin) + 1u);
-          touch(bits, list, &touched, u);
-        } else if (t >= a.vocab) {
-          record_error(a.error_word, kErrIndex);
-        }
-      });
     __syncthreads();
-    const float rep = a.repetition ? a.repetition[s.row] : 1.0f;
-    const float pres = a.presence ? a.presence[s.row] : 0.0f;
-    const float freq = a.frequency ? a.frequency[s.row] : 0.0f;
-    for (uint32_t i = threadIdx.x; i < touched; i += kThreads) {
-      const uint32_t u = list[i], st = state[u], count = st & 0x7FFFFFFFu;
+    for (uint32_t i = threadIdx.x; i < listed; i += kThreads) {
+      const uint32_t u = list[i], made = word[u] & 0x7FFFFFFFu;
       float x = load_elem(src + (s.base + u - 8u));
-      if (a.repetition && st != 0u) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-      if (count != 0u) {
-        if (a.frequency) x = __fsub_rn(x, __fmul_rn(freq, float(count)));
-        if (a.presence) x = __fsub_rn(x, pres);
-      }
-      if (bias && entry[u] != 0u) x = __fadd_rn(x, a.bias_values[bl.begin + entry[u] - 1u]);
-      state[u] = __float_as_uint(__fmul_rn(x, inv_t));
+      x = __fmul_rn(x, x > 0.0f ? row.inv_rep : row.rep);
+      if (made != 0u) x = __fsub_rn(__fsub_rn(x, __fmul_rn(row.freq, float(made))), row.pres);
+      word[u] = __float_as_uint(x);
+      atomicOr(bits + (u >> 5), 1u << (u & 31u));
     }
     __syncthreads();
   }
-  stream_slice(
-      s, src, dst, mask, any ? bits : nullptr, __uint_as_float(0xFF800000u),
-      [&](float x) { return __fmul_rn(x, inv_t); },
-      [&](float, uint32_t u) { return __uint_as_float(state[u]); });
+  if (row.bias.end > row.bias.begin) {
+    // Every warp reads the list backwards, 32 entries at a time, and serves the
+    // places that are its own: the last entry of a token comes first, and the
+    // bit it leaves in `done` turns the others away.
+    uint32_t* done = reinterpret_cast<uint32_t*>(list);
+    for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) done[i] = 0u;
+    __syncthreads();
+    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u, warp = threadIdx.x >> 5;
+    uint32_t bad = 0u;
+    for (int64_t last = row.bias.end; last > row.bias.begin; last -= 32) {
+      const int64_t i = last - 1 - lane;  // the lowest lane has the latest entry
+      const bool have = i >= row.bias.begin;
+      const uint32_t t = have ? uint32_t(a.bias_tokens[i]) : 0xFFFFFFFFu, u = t - s.first + off;
+      bad |= have && t >= a.vocab;
+      const bool own = t - s.first < len && u * (kThreads / 32u) / kPlaces == warp;
+      const uint32_t owners = __ballot_sync(0xFFFFFFFFu, own);
+      if (!own) continue;
+      const uint32_t same = __match_any_sync(owners, u), bit = 1u << (u & 31u);
+      if (lane != uint32_t(__ffs(same) - 1)) continue;
+      if (atomicOr(done + (u >> 5), bit) & bit) continue;
+      const bool seen = (bits[u >> 5] & bit) != 0u;
+      const float x = seen ? __uint_as_float(word[u]) : load_elem(src + (s.base + u - 8u));
+      word[u] = __float_as_uint(__fadd_rn(x, a.bias_values[i]));
+      atomicOr(bits + (u >> 5), bit);
+    }
+    if (bad) record_error(a.error_word, kErrIndex);
+    __syncthreads();
+  }
+  const float inv_t = row.inv_t;
+#pragma unroll
+  for (int r = 0; r < kGroups; ++r) {
+    const uint32_t q = threadIdx.x + r * kThreads;
+    if (q < g.count) {
+      float x[8];
+      values(g.x[r], x);
+      const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
+      if (hit) {
+        const uint4 lo = reinterpret_cast<const uint4*>(word)[2u * q + 2u];
+        const uint4 hi = reinterpret_cast<const uint4*>(word)[2u * q + 3u];
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = (hit >> k) & 1u ? __uint_as_float(w[k]) : x[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], inv_t);
+      store_masked(dst + s.base + 8u * q, x, g.ok[r], kClosed);
+    }
+  }
+  each_single(s, g.count, [&](uint32_t t) {
+    const uint32_t u = t - s.base + 8u;
+    float y = kClosed;
+    if (open_token(mask, t)) {
+      const bool touched = (bits[u >> 5] >> (u & 31u)) & 1u;
+      y = __fmul_rn(touched ? __uint_as_float(word[u]) : load_elem(src + t), inv_t);
+    }
+    store_elem(dst + t, y);
+  });
 }
 
+// Backward: a bit a token of the history, and the raw logits of groups that have one.
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ LogitsArgs a) {
-  extern __shared__ uint4 smem[];
-  __shared__ uint32_t touched;
-  const uint32_t n = places(a.slice);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem);         // a bit per place of the history
-  uint32_t* above = bits + n / 32u;                           // its raw logit is above 0
-  uint16_t* list = reinterpret_cast<uint16_t*>(above + n / 32u);
+__global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __grid_constant__ LogitsArgs a) {
+  __shared__ uint32_t bits[kWords];
+  __shared__ RowSettings row;
   const TOut* src = static_cast<const TOut*>(a.src);
   TIn* dst = static_cast<TIn*>(a.dst);
-  const Slice s = slice_of(a, src, dst);
-  const Range h = a.repetition ? history_of(a, s.row) : Range{0, 0, 0};
+  Slice s = slice_of(a, src, dst);
+  const TIn* raw = static_cast<const TIn*>(a.raw) + (a.raw ? s.row * a.raw_stride : 0u);
+  if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
   const uint32_t* mask = mask_of(a, s.row);
-  const float inv_t = inverse_temperature(a.temperature, s.row);
-  const bool any = h.end > h.begin;
-  float rep = 1.0f;
-  if (any) {
-    rep = a.repetition[s.row];
-    if (threadIdx.x == 0) touched = 0u;
-    for (uint32_t i = threadIdx.x; i < n / 32u; i += kThreads) bits[i] = above[i] = 0u;
-    __syncthreads();
-    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
-    scan_tokens(a.tokens, h.begin, h.end, [&](uint32_t t, int64_t) {
-      if (t - s.first < len)
-        touch(bits, list, &touched, t - s.first + off);
-      else if (t >= a.vocab)
-        record_error(a.error_word, kErrIndex);
+  Groups<TOut> g;
+  g.load(s, src, mask);
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  if (threadIdx.x == 0) read_row(a, s.row, a.tokens && a.repetition, row);
+  __syncthreads();
+  if (row.history.end > row.history.begin) {
+    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t) {
+      if (in) atomicOr(bits + (u >> 5), 1u << (u & 31u));
     });
     __syncthreads();
-    const TIn* raw = static_cast<const TIn*>(a.raw) + s.row * a.raw_stride;
-    for (uint32_t i = threadIdx.x; i < touched; i += kThreads) {
-      const uint32_t u = list[i];
-      if (load_elem(raw + (s.base + u - 8u)) > 0.0f) atomicOr(above + (u >> 5), 1u << (u & 31u));
-    }
-    __syncthreads();
   }
-  stream_slice(
-      s, src, dst, mask, any ? bits : nullptr, 0.0f, [&](float x) { return __fmul_rn(x, inv_t); },
-      [&](float x, uint32_t u) {
-        const float d = __fmul_rn(x, inv_t);
-        return (above[u >> 5] >> (u & 31u)) & 1u ? __fdiv_rn(d, rep) : __fmul_rn(d, rep);
-      });
+  const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
+  Raw<TIn> x[kGroups];
+#pragma unroll
+  for (int r = 0; r < kGroups; ++r) {
+    const uint32_t q = threadIdx.x + r * kThreads;
+    if (g.ok[r] && reinterpret_cast<const uint8_t*>(bits)[q + 1u]) load_group(raw + s.base + 8u * q, x[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kGroups; ++r) {
+    const uint32_t q = threadIdx.x + r * kThreads;
+    if (q < g.count) {
+      const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
+      float d[8];
+      values(g.x[r], d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[k] = __fmul_rn(d[k], inv_t);
+      if (hit) {
+        float v[8];
+        values(x[r], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = (hit >> k) & 1u ? __fmul_rn(d[k], v[k] > 0.0f ? inv_rep : rep) : d[k];
+      }
+      store_masked(dst + s.base + 8u * q, d, g.ok[r], 0.0f);
+    }
+  }
+  each_single(s, g.count, [&](uint32_t t) {
+    const uint32_t u = t - s.base + 8u;
+    float y = 0.0f;
+    if (open_token(mask, t)) {
+      y = __fmul_rn(load_elem(src + t), inv_t);
+      if ((bits[u >> 5] >> (u & 31u)) & 1u) y = __fmul_rn(y, load_elem(raw + t) > 0.0f ? inv_rep : rep);
+    }
+    store_elem(dst + t, y);
+  });
 }
 
-// Slices of a row: the largest that still gives every SM several CTAs, since a
-// slice costs one more reading of the history.
-void cut_rows(LogitsArgs& a, uint32_t most, int sms) {
-  uint32_t slice = most;
-  while (slice > kSliceMin && a.rows * ((a.vocab + slice - 1) / slice) < uint64_t(sms) * 4) slice /= 2;
-  a.slices = (a.vocab + slice - 1) / slice;
-  a.slice = slice;
+// Slices of a row: as few as possible, since every one reads the history, but
+// more where there are too few rows to give every SM two CTAs.
+void cut_rows(LogitsArgs& a, int sms) {
+  uint32_t k = (a.vocab + kSliceMax - 1) / kSliceMax;
+  while (a.rows * k < uint64_t(sms) * 2 && a.vocab / (2 * k) >= kSliceMin) k *= 2;
+  a.slices = k;
+  a.slice = ((a.vocab + k - 1) / k + 7u) & ~7u;
 }
 
 template <typename K>
-cudaError_t launch(K kernel, const LogitsArgs& a, uint32_t smem, cudaStream_t stream) {
-  if (smem > 48u * 1024u) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<unsigned(a.rows * a.slices), kThreads, smem, stream>>>(a);
+cudaError_t launch_full(K kernel, const LogitsArgs& a, cudaStream_t stream) {
+  constexpr uint32_t kBytes = kPlaces * 6u;  // word, list
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBytes));
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(a.rows * a.slices), kThreads, kBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_logits_shape(LogitsArgs a, int in_type, int out_type, int sms, cudaStream_t stream) {
-  cut_rows(a, PULSE_LOGITS_SLICE, sms);
-  const bool history = a.tokens && (a.repetition || a.presence || a.frequency);
-  const uint32_t n = places(a.slice);
-  uint32_t smem = 0;
-  if (history || a.bias_tokens) smem = n / 8u + n * 6u + (a.bias_tokens ? n * 4u : 0u);
-  if (in_type == PULSE_F32) return launch(shape_kernel<float, float>, a, smem, stream);
-  if (out_type == PULSE_F32) return launch(shape_kernel<uint16_t, float>, a, smem, stream);
-  return launch(shape_kernel<uint16_t, uint16_t>, a, smem, stream);
+  cut_rows(a, sms);
+  if (a.bias_tokens || (a.tokens && (a.presence || a.frequency))) {
+    if (in_type == PULSE_F32) return launch_full(shape_kernel<float, float>, a, stream);
+    if (out_type == PULSE_F32) return launch_full(shape_kernel<uint16_t, float>, a, stream);
+    return launch_full(shape_kernel<uint16_t, uint16_t>, a, stream);
+  }
+  const unsigned grid = unsigned(a.rows * a.slices);
+  if (in_type == PULSE_F32)
+    scale_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
+  else if (out_type == PULSE_F32)
+    scale_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
+  else
+    scale_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_logits_backward(LogitsArgs a, int in_type, int out_type, int sms,
                                    cudaStream_t stream) {
-  cut_rows(a, PULSE_LOGITS_SLICE_BACK, sms);
-  const uint32_t n = places(a.slice);
-  const uint32_t smem = a.tokens && a.repetition ? n / 4u + n * 2u : 0u;
-  if (in_type == PULSE_F32) return launch(backward_kernel<float, float>, a, smem, stream);
-  if (out_type == PULSE_F32) return launch(backward_kernel<uint16_t, float>, a, smem, stream);
-  return launch(backward_kernel<uint16_t, uint16_t>, a, smem, stream);
+  cut_rows(a, sms);
+  const unsigned grid = unsigned(a.rows * a.slices);
+  if (in_type == PULSE_F32)
+    backward_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
+  else if (out_type == PULSE_F32)
+    backward_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
+  else
+    backward_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace pulse
