@@ -1764,21 +1764,46 @@ bool rows_ok(const RowsOf& r, uint64_t vocab) {
          aligned(r.p, uintptr_t(elem_bytes(r.type)));
 }
 
-// Fills the shaping's part and the stream's error word.
-int logits_args(const pulse_logits_shaping& s, uint64_t rows, cudaStream_t stream, LogitsArgs* a, int* sms) {
+// Sorted histories of one stream (kernels on it run in order, so calls share it).
+struct LogitsWorkspace {
+  uint32_t* entries = nullptr;
+  uint16_t* offs = nullptr;
+  uint64_t entry_cap = 0, offs_cap = 0;
+};
+std::map<std::pair<int, uintptr_t>, LogitsWorkspace*> g_logits_ws;
+
+// Room for a call's sorted histories; growth synchronises `stream`. Returns false
+// where there is none (no memory, or the stream is being captured): the call then
+// works on the unsorted tokens.
+bool logits_reserve(LogitsWorkspace& w, uint64_t entries, uint64_t offs, cudaStream_t stream) {
+  if (entries <= w.entry_cap && offs <= w.offs_cap) return true;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return false;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return false;
+  if (w.entries) cudaFree(w.entries);
+  if (w.offs) cudaFree(w.offs);
+  const uint64_t ne = entries + entries / 4, no = offs + offs / 4;
+  w = LogitsWorkspace{};
+  if (cudaMalloc(&w.entries, ne * sizeof(uint32_t)) != cudaSuccess ||
+      cudaMalloc(&w.offs, no * sizeof(uint16_t)) != cudaSuccess) {
+    if (w.entries) cudaFree(w.entries);
+    w = LogitsWorkspace{};
+    cudaGetLastError();
+    return false;
+  }
+  w.entry_cap = ne;
+  w.offs_cap = no;
+  return true;
+}
+
+// Fills the shaping's part and the stream's error word, and sorts the tokens
+// where `history` is read and the sorting pays.
+int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cudaStream_t stream,
+                LogitsArgs* a) {
   // one CTA per slice of a row: the grid has to fit its 31 bits
   if (rows > kMaxTiles / div_up(s.vocab, 1024)) return PULSE_ERR_RANGE;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
-  *sms = sm_count(device);
-  {
-    std::lock_guard<std::mutex> lock(g_ws_mu);
-    Workspace* ws = stream_workspace(device, stream);
-    if (ws == nullptr) return PULSE_ERR_NOMEM;
-    const int st = workspace_reserve(*ws, 0, stream);
-    if (st != PULSE_OK) return st;
-    a->error_word = ws->counters + 2;
-  }
   a->rows = rows;
   a->vocab = uint32_t(s.vocab);
   a->tokens = s.tokens;
@@ -1798,7 +1823,22 @@ int logits_args(const pulse_logits_shaping& s, uint64_t rows, cudaStream_t strea
   a->mask_rows = int64_t(s.mask_rows);
   a->mask_stride = s.mask_stride;
   a->mask_row = s.mask_row;
-  return PULSE_OK;
+  const int sms = sm_count(device);
+  logits_cut(*a, sms);
+  std::lock_guard<std::mutex> lock(g_ws_mu);
+  Workspace* ws = stream_workspace(device, stream);
+  if (ws == nullptr) return PULSE_ERR_NOMEM;
+  const int st = workspace_reserve(*ws, 0, stream);
+  if (st != PULSE_OK) return st;
+  a->error_word = ws->counters + 2;
+  if (!history || !logits_sorts(*a, sms)) return PULSE_OK;
+  LogitsWorkspace*& lw = g_logits_ws[std::make_pair(device, reinterpret_cast<uintptr_t>(stream))];
+  if (lw == nullptr) lw = new (std::nothrow) LogitsWorkspace();
+  if (lw == nullptr) return PULSE_ERR_NOMEM;
+  if (!logits_reserve(*lw, logits_sort_entries(*a), logits_sort_offs(*a), stream)) return PULSE_OK;
+  a->sorted = lw->entries;
+  a->sorted_offs = lw->offs;
+  return cuda_status(launch_logits_sort(*a, lw->entries, lw->offs, stream));
 }
 
 }  // namespace
@@ -1813,14 +1853,14 @@ int pulse_logits_shape(const pulse_logits_shaping* shaping, uint64_t rows, const
   if (!rows_ok(src, shaping->vocab) || !rows_ok(dst, shaping->vocab)) return PULSE_ERR_INVALID;
   if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
   LogitsArgs a{};
-  int sms = 0;
-  const int st = logits_args(*shaping, rows, stream, &a, &sms);
+  const bool history = shaping->tokens && (shaping->repetition || shaping->presence || shaping->frequency);
+  const int st = logits_args(*shaping, rows, history, stream, &a);
   if (st != PULSE_OK) return st;
   a.src = logits;
   a.src_stride = stride;
   a.dst = out;
   a.dst_stride = out_stride;
-  return cuda_status(launch_logits_shape(a, in_type, out_type, sms, stream));
+  return cuda_status(launch_logits_shape(a, in_type, out_type, stream));
 }
 
 int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t rows, const void* dout,
@@ -1838,8 +1878,7 @@ int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t ro
     return PULSE_ERR_INVALID;
   if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
   LogitsArgs a{};
-  int sms = 0;
-  const int st = logits_args(*shaping, rows, stream, &a, &sms);
+  const int st = logits_args(*shaping, rows, needs_raw, stream, &a);
   if (st != PULSE_OK) return st;
   a.src = dout;
   a.src_stride = dout_stride;
@@ -1847,7 +1886,7 @@ int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t ro
   a.raw_stride = stride;
   a.dst = dlogits;
   a.dst_stride = dlogits_stride;
-  return cuda_status(launch_logits_backward(a, in_type, out_type, sms, stream));
+  return cuda_status(launch_logits_backward(a, in_type, out_type, stream));
 }
 
 }  // extern "C"

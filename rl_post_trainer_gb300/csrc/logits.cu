@@ -14,7 +14,7 @@ namespace pulse {
 namespace {
 
 #ifndef PULSE_LOGITS_MIN
-#define PULSE_LOGITS_MIN 4
+#define PULSE_LOGITS_MIN 5
 #endif
 #ifndef PULSE_LOGITS_GROUPS
 #define PULSE_LOGITS_GROUPS 4
@@ -87,26 +87,63 @@ struct Range {
   int64_t begin, split, end;
 };
 
-// The row's history, empty (and recorded) where its offsets do not fit.
-__device__ __forceinline__ Range history_of(const LogitsArgs& a, uint64_t row) {
-  const int64_t b = a.begin[row], e = a.end[row];
-  const int64_t s = a.split ? a.split[row] : b;
-  if (b >= 0 && s >= b && e >= s && e <= a.ntokens) return {b, s, e};
-  record_error(a.error_word, kErrIndex);
-  return {0, 0, 0};
+// What a warp asks for of its row before anything else: a setting a lane, so that
+// one wait covers them all.
+struct RowLoads {
+  int64_t v8;
+  float v4;
+  int32_t mask_row;
+};
+__device__ __forceinline__ RowLoads load_row(const LogitsArgs& a, uint32_t row, bool history) {
+  const uint32_t lane = threadIdx.x & 31u;
+  const int64_t* p8 = nullptr;
+  const float* p4 = nullptr;
+  if (history) {
+    if (lane == 0) p8 = a.begin + row;
+    if (lane == 1) p8 = (a.split ? a.split : a.begin) + row;
+    if (lane == 2) p8 = a.end + row;
+  }
+  if (a.bias_tokens && (lane == 3 || lane == 4)) p8 = a.bias_begin + row + (lane - 3u);
+  if (lane == 5) p4 = a.repetition;
+  if (lane == 6) p4 = a.temperature;
+  if (lane == 7) p4 = a.presence;
+  if (lane == 8) p4 = a.frequency;
+  RowLoads r;
+  r.v8 = p8 ? *p8 : 0;
+  r.v4 = p4 ? p4[row] : lane < 7 ? 1.0f : 0.0f;
+  r.mask_row = a.mask == nullptr ? -1 : a.mask_row ? a.mask_row[row] : int32_t(row);
+  return r;
 }
 
-__device__ __forceinline__ Range bias_of(const LogitsArgs& a, uint64_t row) {
-  const int64_t b = a.bias_begin[row], e = a.bias_begin[row + 1];
-  if (b >= 0 && e >= b && e <= a.nbias) return {b, b, e};
-  record_error(a.error_word, kErrIndex);
-  return {0, 0, 0};
+// The row's settings. Ranges that do not fit their lists are empty (and recorded).
+struct RowSettings {
+  Range history, bias;
+  float rep, inv_rep, pres, freq, inv_t;
+};
+__device__ __forceinline__ RowSettings settings_of(const LogitsArgs& a, const RowLoads& l, bool history) {
+  auto i64 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, l.v8, k); };
+  auto f32 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, l.v4, k); };
+  RowSettings r;
+  r.history = Range{i64(0), i64(1), i64(2)};
+  r.bias = Range{i64(3), i64(3), i64(4)};
+  const bool h_ok = r.history.begin >= 0 && r.history.split >= r.history.begin &&
+                    r.history.end >= r.history.split && r.history.end <= a.ntokens;
+  const bool b_ok = r.bias.begin >= 0 && r.bias.end >= r.bias.begin && r.bias.end <= a.nbias;
+  if (!h_ok) r.history = Range{0, 0, 0};
+  if (!b_ok) r.bias = Range{0, 0, 0};
+  if (((history && !h_ok) || (a.bias_tokens && !b_ok)) && threadIdx.x == 0) record_error(a.error_word, kErrIndex);
+  const float t = f32(6);
+  r.rep = f32(5);
+  r.inv_rep = __frcp_rn(r.rep);
+  r.inv_t = t > 0.0f ? __frcp_rn(t) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
+  r.pres = f32(7);
+  r.freq = f32(8);
+  return r;
 }
 
 // The row's mask words, or null.
-__device__ __forceinline__ const uint32_t* mask_of(const LogitsArgs& a, uint64_t row) {
-  if (a.mask == nullptr) return nullptr;
-  const int64_t m = a.mask_row ? int64_t(a.mask_row[row]) : int64_t(row);
+__device__ __forceinline__ const uint32_t* mask_of(const LogitsArgs& a, const RowLoads& l) {
+  const int32_t m = l.mask_row;
   if (m < 0) return nullptr;
   if (m >= a.mask_rows) {
     if (threadIdx.x == 0) record_error(a.error_word, kErrIndex);
@@ -115,18 +152,11 @@ __device__ __forceinline__ const uint32_t* mask_of(const LogitsArgs& a, uint64_t
   return a.mask + uint64_t(m) * a.mask_stride;
 }
 
-// The 8 mask bits from token t on; a group that ends inside the vocabulary.
-__device__ __forceinline__ uint32_t mask_bits8(const uint32_t* mask, uint32_t t) {
-  const uint32_t w = t >> 5, s = t & 31u;
-  const uint32_t lo = mask[w], hi = s > 24u ? mask[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, s) & 0xFFu;
-}
-
-// This CTA's part of a row: tokens [first, stop), groups from `base` on. Token t
-// has place t - base + 8, so that a group's bits are a byte of the bitmap and the
-// tokens in front of the first group (row start) have places below 8.
+// This CTA's part of a row: tokens [first, stop), groups from `base` on, up to 7
+// tokens later. Token t has place t - base + 8, so that a group's bits are a byte
+// of the bitmap and the tokens in front of the first group have places below 8.
 struct Slice {
-  uint32_t row;
+  uint32_t row, index;
   uint32_t first, base, stop;
   bool grouped;  // all rows involved share their group boundaries
 };
@@ -135,80 +165,213 @@ template <typename TSrc, typename TDst>
 __device__ __forceinline__ Slice slice_of(const LogitsArgs& a, const TSrc*& src, TDst*& dst) {
   Slice s;
   s.row = blockIdx.x / a.slices;
-  const uint32_t k = blockIdx.x % a.slices;
+  s.index = blockIdx.x % a.slices;
   src += s.row * a.src_stride;
   dst += s.row * a.dst_stride;
-  uint32_t lead = lead_of(src);
+  s.first = s.index * a.slice;  // a multiple of 32
+  s.stop = min(s.first + a.slice, a.vocab);
+  const uint32_t lead = lead_of(src);
   s.grouped = lead == lead_of(dst);
-  if (!s.grouped) lead = 0u;
-  s.base = lead + k * a.slice;
-  s.first = k == 0 ? 0u : min(s.base, a.vocab);
-  s.stop = k + 1 == a.slices ? a.vocab : min(s.base + a.slice, a.vocab);
+  s.base = s.first + (s.grouped ? lead : 0u);
   return s;
 }
 
-// Calls f(in, place, position) for the entries [begin, end) of a list of tokens,
-// a warp's lanes together; `in`: the entry belongs to the slice. Calls in which no
-// lane has one are left out: with a dozen slices a row that is most of them. Tokens
-// outside the vocabulary are recorded.
+// Four entries a lane of a list of tokens: which of them belong to the slice, at
+// which place, and which were generated.
+struct Four {
+  bool in[4], made[4];
+  uint32_t u[4];
+};
+
+// Calls f(four) for the history, a warp's lanes together. Calls in which no lane has
+// an entry of the slice are left out: with a dozen slices a row that is most of
+// them. Tokens outside the vocabulary are recorded.
 template <typename F>
-__device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s, const int32_t* tokens,
-                                            int64_t begin, int64_t end, F f) {
-  const int32_t* p = tokens + begin;
+__device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
+  const int32_t* p = a.tokens + h.begin;
   const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
-  const uint32_t vocab = a.vocab;
   uint32_t bad = 0u;
-  auto one = [&](uint32_t t, int64_t i) {
-    const bool in = t - s.first < len;
-    bad |= t >= vocab;
-    if (__any_sync(0xFFFFFFFFu, in)) f(in, t - s.first + off, i);
+  auto four = [&](const int4& t, int64_t i, bool have) {
+    const uint32_t v[4] = {uint32_t(t.x), uint32_t(t.y), uint32_t(t.z), uint32_t(t.w)};
+    Four x;
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x.in[k] = have && v[k] - s.first < len;
+      x.made[k] = i + k >= h.split;
+      x.u[k] = v[k] - s.first + off;
+      bad |= have && v[k] >= a.vocab;
+      any |= x.in[k];
+    }
+    if (__any_sync(0xFFFFFFFFu, any)) f(x);
   };
-  const int64_t n = end - begin;
+  const int64_t n = h.end - h.begin;
   const int64_t lead = min(n, int64_t((0u - uint32_t(reinterpret_cast<uintptr_t>(p) / 4u)) & 3u));
   const int64_t quads = (n - lead) / 4, rest = lead + 4 * quads;
   const int4* quad = reinterpret_cast<const int4*>(p + lead);
-  for (int64_t q = threadIdx.x & ~31u; q < quads; q += kThreads) {
-    const int64_t at = q + (threadIdx.x & 31u);
-    int4 t = make_int4(-1, -1, -1, -1);
-    const bool have = at < quads;
-    if (have) t = __ldg(quad + at);
-    const int64_t i = begin + lead + 4 * at;
-    const uint32_t before = bad;
-    one(uint32_t(t.x), i);
-    one(uint32_t(t.y), i + 1);
-    one(uint32_t(t.z), i + 2);
-    one(uint32_t(t.w), i + 3);
-    if (!have) bad = before;
+  const int4 none = make_int4(-1, -1, -1, -1);
+  int64_t at = threadIdx.x;
+  int4 next = at < quads ? __ldg(quad + at) : none;
+  for (int64_t q = threadIdx.x & ~31u; q < quads; q += kThreads, at += kThreads) {
+    const int4 t = next;
+    next = at + kThreads < quads ? __ldg(quad + at + kThreads) : none;
+    four(t, h.begin + lead + 4 * at, at < quads);
   }
-  // up to 3 entries in front of the aligned ones and 3 behind, by the first warp
+  // up to 3 entries in front of the aligned ones and 3 behind, one a lane of the first warp
   if (threadIdx.x < 32u) {
     const int64_t i = threadIdx.x < lead ? threadIdx.x : rest + (threadIdx.x - lead);
-    const bool have = i < n;
-    const uint32_t before = bad;
-    one(have ? uint32_t(p[i]) : 0xFFFFFFFFu, begin + i);
-    if (!have) bad = before;
+    const uint32_t t = i < n ? uint32_t(p[i]) : 0xFFFFFFFFu;
+    bad |= i < n && t >= a.vocab;
+    Four x{};
+    x.in[0] = t - s.first < len;
+    x.made[0] = h.begin + i >= h.split;
+    x.u[0] = t - s.first + off;
+    f(x);
   }
   if (bad) record_error(a.error_word, kErrIndex);
 }
 
-// This thread's groups of a slice. Masked tokens are not read where a whole group
-// is masked.
+// ---- histories sorted by slice
+//
+// Every slice of a row reads the row's whole history, which for long histories is
+// most of the work. With enough rows the token list is therefore sorted first:
+// block by block of kBlock tokens, the tokens of one slice side by side. A slice
+// then reads its own part of the blocks its history touches.
+constexpr uint32_t kBlock = 2048;
+constexpr uint32_t kSortSlices = 250;  // most slices that are sorted for
+
+// entries: place in the slice's vocabulary | position in the block << 16; offs:
+// for every block, where each slice's entries begin (slices + 2 words; the slice
+// past the last holds tokens outside the vocabulary).
+__global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64_t ntokens, uint32_t vocab,
+                                                   uint32_t slice, uint32_t slices, uint32_t* entries,
+                                                   uint16_t* offs) {
+  __shared__ uint32_t count[256];
+  __shared__ uint32_t begin[256];
+  constexpr int kEach = kBlock / 256;
+  const uint64_t base = uint64_t(blockIdx.x) * kBlock;
+  count[threadIdx.x] = 0u;
+  uint32_t token[kEach], bucket[kEach], place[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const uint64_t i = base + threadIdx.x + 256 * k;
+    token[k] = i < ntokens ? uint32_t(tokens[i]) : 0xFFFFFFFFu;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    bucket[k] = token[k] < vocab ? token[k] / slice : slices;
+    token[k] -= token[k] < vocab ? bucket[k] * slice : token[k];
+    place[k] = atomicAdd(count + bucket[k], 1u);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    uint32_t sum = 0u;
+    for (uint32_t w = 0; w < 256; w += 32) {
+      const uint32_t own = count[w + threadIdx.x];
+      uint32_t x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (threadIdx.x >= uint32_t(o)) x += y;
+      }
+      begin[w + threadIdx.x] = sum + x - own;
+      sum += __shfl_sync(0xFFFFFFFFu, x, 31);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < slices + 2u) offs[uint64_t(blockIdx.x) * (slices + 2u) + threadIdx.x] = uint16_t(begin[threadIdx.x]);
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    entries[base + begin[bucket[k]] + place[k]] = token[k] | ((threadIdx.x + 256u * k) << 16);
+}
+
+// As scan_tokens, of sorted tokens.
+template <typename F>
+__device__ __forceinline__ void scan_sorted(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, row = a.slices + 2u;
+  const uint32_t b0 = uint32_t(h.begin / kBlock), blocks = uint32_t((h.end - 1) / kBlock) - b0 + 1u;
+  // warps share a block where there are fewer blocks than warps
+  constexpr uint32_t kWarps = kThreads / 32;
+  uint32_t share = 1u;
+  while (share * 2u * blocks <= kWarps) share *= 2u;
+  const uint32_t off = s.first - s.base + 8u, part = warp % share;
+  uint32_t bad = 0u;
+  for (uint32_t b = warp / share; b < blocks; b += kWarps / share) {
+    const int64_t base = int64_t(b0 + b) * kBlock;
+    const uint16_t* o = a.sorted_offs + uint64_t(b0 + b) * row + s.index;
+    const uint32_t* e = a.sorted + base;
+    const uint32_t lo = o[0], hi = o[1];
+    // the history's part of the block, and where its generated part starts
+    const uint32_t from = uint32_t(max(h.begin - base, int64_t(0))), to = uint32_t(min(h.end - base, int64_t(kBlock)));
+    const uint32_t made = uint32_t(min(max(h.split - base, int64_t(0)), int64_t(kBlock)));
+    if (s.index == 0u && part == 0u)  // tokens outside the vocabulary, among the row's
+      for (uint32_t i = o[a.slices] + lane; i < o[a.slices + 1u]; i += 32u) bad |= (e[i] >> 16) - from < to - from;
+    for (uint32_t i = lo + part * 128u; i < hi; i += share * 128u) {
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = i + lane + 32u * k < hi ? e[i + lane + 32u * k] : 0xFFFF0000u;
+      Four x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t at = v[k] >> 16;
+        x.in[k] = at - from < to - from;
+        x.made[k] = at >= made;
+        x.u[k] = (v[k] & 0xFFFFu) + off;
+      }
+      f(x);
+    }
+  }
+  if (bad) record_error(a.error_word, kErrIndex);
+}
+
+template <typename F>
+__device__ __forceinline__ void scan_history(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
+  if (a.sorted)
+    scan_sorted(a, s, h, f);
+  else
+    scan_tokens(a, s, h, f);
+}
+
+// Sets the bits of the history.
+__device__ __forceinline__ void mark_history(const LogitsArgs& a, const Slice& s, const Range& h, uint32_t* bits) {
+  scan_history(a, s, h, [&](const Four& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x.in[k]) atomicOr(bits + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
+  });
+}
+
+// The slice's mask words, copied to shared memory while other things go on;
+// mask_ready() before the barrier after which they are read.
+__device__ __forceinline__ void copy_mask(const uint32_t* mask, const Slice& s, uint32_t* words) {
+  if (mask == nullptr) return;
+  const uint32_t n = (s.stop - s.first + 31u) / 32u;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(words + i)), "l"(mask + s.first / 32u + i)
+                 : "memory");
+}
+__device__ __forceinline__ void mask_ready() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The bits of the 8 tokens from t on, a group that ends inside the slice.
+__device__ __forceinline__ uint32_t mask_bits8(const uint32_t* words, const Slice& s, uint32_t t) {
+  const uint32_t i = t - s.first;
+  return __funnelshift_r(words[i >> 5], words[(i + 7u) >> 5], i & 31u) & 0xFFu;
+}
+
+// This thread's groups of a slice.
 template <typename TSrc>
 struct Groups {
   Raw<TSrc> x[kGroups];
-  uint32_t ok[kGroups];  // a bit a token: open (0 past the slice)
-  uint32_t count;        // of the slice
+  uint32_t count;  // of the slice
 
-  __device__ __forceinline__ void load(const Slice& s, const TSrc* src, const uint32_t* mask) {
+  __device__ __forceinline__ void load(const Slice& s, const TSrc* src) {
     count = s.grouped && s.stop > s.base ? (s.stop - s.base) / 8u : 0u;
 #pragma unroll
     for (int r = 0; r < kGroups; ++r) {
       const uint32_t q = threadIdx.x + r * kThreads;
-      ok[r] = q >= count ? 0u : mask ? mask_bits8(mask, s.base + 8u * q) : 0xFFu;
+      if (q < count) load_group(src + s.base + 8u * q, x[r]);
     }
-#pragma unroll
-    for (int r = 0; r < kGroups; ++r)
-      if (ok[r]) load_group(src + s.base + 8u * (threadIdx.x + r * kThreads), x[r]);
   }
 };
 
@@ -236,49 +399,33 @@ __device__ __forceinline__ void each_single(const Slice& s, uint32_t groups, F f
   if (s.stop > s.base && tail < s.stop) f(tail);
 }
 
-__device__ __forceinline__ bool open_token(const uint32_t* mask, uint32_t t) {
-  return mask == nullptr || ((mask[t >> 5] >> (t & 31u)) & 1u);
+__device__ __forceinline__ bool open_token(const uint32_t* mask, const uint32_t* words, const Slice& s, uint32_t t) {
+  return mask == nullptr || ((words[(t - s.first) >> 5] >> (t & 31u)) & 1u);
 }
 
 constexpr float kClosed = -__builtin_huge_valf();
 
-// What thread 0 reads of the row for all.
-struct RowSettings {
-  Range history, bias;
-  float rep, inv_rep, pres, freq, inv_t;
-};
-
-__device__ __forceinline__ void read_row(const LogitsArgs& a, uint32_t row, bool history, RowSettings& r) {
-  r.history = history ? history_of(a, row) : Range{0, 0, 0};
-  r.bias = a.bias_tokens ? bias_of(a, row) : Range{0, 0, 0};
-  r.rep = a.repetition ? a.repetition[row] : 1.0f;
-  r.inv_rep = __frcp_rn(r.rep);
-  r.pres = a.presence ? a.presence[row] : 0.0f;
-  r.freq = a.frequency ? a.frequency[row] : 0.0f;
-  const float t = a.temperature ? a.temperature[row] : 1.0f;
-  r.inv_t = t > 0.0f ? __frcp_rn(t) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
-}
-
 // Repetition penalty and temperature alone: a bit a token is all there is to keep.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_constant__ LogitsArgs a) {
-  __shared__ uint32_t bits[kWords];
-  __shared__ RowSettings row;
+  __shared__ uint32_t bits[kWords], open[kWords];
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
   const Slice s = slice_of(a, src, dst);
-  const uint32_t* mask = mask_of(a, s.row);
+  const bool history = a.tokens && a.repetition;
+  const RowLoads loads = load_row(a, s.row, history);
   Groups<TIn> g;
-  g.load(s, src, mask);
+  g.load(s, src);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
-  if (threadIdx.x == 0) read_row(a, s.row, a.tokens && a.repetition, row);
-  __syncthreads();
+  const uint32_t* mask = mask_of(a, loads);
+  copy_mask(mask, s, open);
+  const RowSettings row = settings_of(a, loads, history);
   if (row.history.end > row.history.begin) {
-    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t) {
-      if (in) atomicOr(bits + (u >> 5), 1u << (u & 31u));
-    });
     __syncthreads();
+    mark_history(a, s, row.history, bits);
   }
+  mask_ready();
+  __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
   auto seen = [&](float x) { return __fmul_rn(__fmul_rn(x, x > 0.0f ? inv_rep : rep), inv_t); };
 #pragma unroll
@@ -294,13 +441,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = (hit >> k) & 1u ? seen(x[k]) : y[k];
       }
-      store_masked(dst + s.base + 8u * q, y, g.ok[r], kClosed);
+      const uint32_t t = s.base + 8u * q;
+      store_masked(dst + t, y, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = kClosed;
-    if (open_token(mask, t)) {
+    if (open_token(mask, open, s, t)) {
       const float x = load_elem(src + t);
       y = (bits[u >> 5] >> (u & 31u)) & 1u ? seen(x) : __fmul_rn(x, inv_t);
     }
@@ -311,81 +459,78 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_
 // Everything: tokens are counted and biased.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_constant__ LogitsArgs a) {
-  extern __shared__ uint4 smem[];
   // a word a place: bit 31 for a token of the prompt, below it the times it was
-  // generated; then the logit as the penalties and the bias leave it
-  uint32_t* word = reinterpret_cast<uint32_t*>(smem);
-  uint16_t* list = reinterpret_cast<uint16_t*>(word + kPlaces);  // places of the history, each once
-  __shared__ uint32_t bits[kWords];                              // places whose word is a logit
-  __shared__ uint32_t listed;
-  __shared__ RowSettings row;
+  // generated; where its bit in `final` is set, the logit with penalties and bias
+  __shared__ __align__(16) uint32_t word[kPlaces];
+  __shared__ uint32_t final[kWords], open[kWords];
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
   const Slice s = slice_of(a, src, dst);
-  const uint32_t* mask = mask_of(a, s.row);
+  const bool history = a.tokens && (a.repetition || a.presence || a.frequency);
+  const RowLoads loads = load_row(a, s.row, history);
   Groups<TIn> g;
-  g.load(s, src, mask);
-  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  g.load(s, src);
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (threadIdx.x == 0) {
-    listed = 0u;
-    read_row(a, s.row, a.tokens && (a.repetition || a.presence || a.frequency), row);
-  }
+  const uint32_t* mask = mask_of(a, loads);
+  copy_mask(mask, s, open);
+  const RowSettings row = settings_of(a, loads, history);
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  // Every warp reads the bias list backwards, 32 entries at a time, and serves the
+  // places that are its own: the last entry of a token comes first, and its bit in
+  // `final` turns the others away. The latest entries are asked for before the
+  // history is read.
+  constexpr int kAhead = 4;
+  const int64_t biased = row.bias.end - row.bias.begin;
+  uint32_t ahead[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    ahead[k] = int64_t(lane + 32 * k) < biased ? uint32_t(a.bias_tokens[row.bias.end - 1 - lane - 32 * k]) : 0xFFFFFFFFu;
   __syncthreads();
-  const uint32_t lane = threadIdx.x & 31u;
+  auto penalized = [&](float x, uint32_t st) {
+    const uint32_t made = st & 0x7FFFFFFFu;
+    x = __fmul_rn(x, x > 0.0f ? row.inv_rep : row.rep);
+    return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(row.freq, float(made))), row.pres);
+  };
   if (row.history.end > row.history.begin) {
-    const int64_t split = row.history.split;
-    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t i) {
-      uint32_t old = 1u;
-      if (in) old = i >= split ? atomicAdd(word + u, 1u) : atomicOr(word + u, 0x80000000u);
-      const uint32_t fresh = __ballot_sync(0xFFFFFFFFu, old == 0u);
-      if (fresh) {
-        uint32_t at = 0u;
-        if (lane == 0) at = atomicAdd(&listed, uint32_t(__popc(fresh)));
-        at = __shfl_sync(0xFFFFFFFFu, at, 0);
-        if (old == 0u) list[at + __popc(fresh & lanemask_lt())] = uint16_t(u);
-      }
+    scan_history(a, s, row.history, [&](const Four& x) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x.in[k]) {
+          if (x.made[k])
+            atomicAdd(word + x.u[k], 1u);
+          else
+            atomicOr(word + x.u[k], 0x80000000u);
+        }
     });
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < listed; i += kThreads) {
-      const uint32_t u = list[i], made = word[u] & 0x7FFFFFFFu;
-      float x = load_elem(src + (s.base + u - 8u));
-      x = __fmul_rn(x, x > 0.0f ? row.inv_rep : row.rep);
-      if (made != 0u) x = __fsub_rn(__fsub_rn(x, __fmul_rn(row.freq, float(made))), row.pres);
-      word[u] = __float_as_uint(x);
-      atomicOr(bits + (u >> 5), 1u << (u & 31u));
-    }
-    __syncthreads();
+    if (biased > 0) __syncthreads();
   }
-  if (row.bias.end > row.bias.begin) {
-    // Every warp reads the list backwards, 32 entries at a time, and serves the
-    // places that are its own: the last entry of a token comes first, and the
-    // bit it leaves in `done` turns the others away.
-    uint32_t* done = reinterpret_cast<uint32_t*>(list);
-    for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) done[i] = 0u;
-    __syncthreads();
-    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u, warp = threadIdx.x >> 5;
+  if (biased > 0) {
+    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
     uint32_t bad = 0u;
-    for (int64_t last = row.bias.end; last > row.bias.begin; last -= 32) {
-      const int64_t i = last - 1 - lane;  // the lowest lane has the latest entry
-      const bool have = i >= row.bias.begin;
-      const uint32_t t = have ? uint32_t(a.bias_tokens[i]) : 0xFFFFFFFFu, u = t - s.first + off;
-      bad |= have && t >= a.vocab;
+    auto serve = [&](uint32_t t, int64_t i) {  // a warp's lanes together; the lowest has the latest entry
+      bad |= i >= row.bias.begin && t >= a.vocab;
+      const uint32_t u = t - s.first + off;
       const bool own = t - s.first < len && u * (kThreads / 32u) / kPlaces == warp;
       const uint32_t owners = __ballot_sync(0xFFFFFFFFu, own);
-      if (!own) continue;
+      if (!own) return;
       const uint32_t same = __match_any_sync(owners, u), bit = 1u << (u & 31u);
-      if (lane != uint32_t(__ffs(same) - 1)) continue;
-      if (atomicOr(done + (u >> 5), bit) & bit) continue;
-      const bool seen = (bits[u >> 5] & bit) != 0u;
-      const float x = seen ? __uint_as_float(word[u]) : load_elem(src + (s.base + u - 8u));
-      word[u] = __float_as_uint(__fadd_rn(x, a.bias_values[i]));
-      atomicOr(bits + (u >> 5), bit);
-    }
+      if (lane != uint32_t(__ffs(same) - 1)) return;
+      if (atomicOr(final + (u >> 5), bit) & bit) return;
+      const float x = load_elem(src + (s.base + u - 8u));
+      word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, a.bias_values[i]));
+    };
+    int64_t i = row.bias.end - 1 - lane;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k, i -= 32)
+      if (biased > 32 * k) serve(ahead[k], i);
+    for (int64_t left = biased - 32 * kAhead; left > 0; left -= 32, i -= 32)
+      serve(i >= row.bias.begin ? uint32_t(a.bias_tokens[i]) : 0xFFFFFFFFu, i);
     if (bad) record_error(a.error_word, kErrIndex);
-    __syncthreads();
   }
+  mask_ready();
+  __syncthreads();
   const float inv_t = row.inv_t;
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
@@ -393,25 +538,36 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
     if (q < g.count) {
       float x[8];
       values(g.x[r], x);
-      const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
-      if (hit) {
-        const uint4 lo = reinterpret_cast<const uint4*>(word)[2u * q + 2u];
-        const uint4 hi = reinterpret_cast<const uint4*>(word)[2u * q + 3u];
-        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const uint32_t fin = reinterpret_cast<const uint8_t*>(final)[q + 1u];
+      const uint4 lo = reinterpret_cast<const uint4*>(word)[2u * q + 2u];
+      const uint4 hi = reinterpret_cast<const uint4*>(word)[2u * q + 3u];
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      if ((w[0] | w[1] | w[2]) | (w[3] | w[4] | w[5]) | (w[6] | w[7] | fin)) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = (hit >> k) & 1u ? __uint_as_float(w[k]) : x[k];
+        for (int k = 0; k < 8; ++k) {
+          if (w[k]) x[k] = penalized(x[k], w[k]);
+        }
+        if (fin) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = (fin >> k) & 1u ? __uint_as_float(w[k]) : x[k];
+        }
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], inv_t);
-      store_masked(dst + s.base + 8u * q, x, g.ok[r], kClosed);
+      const uint32_t t = s.base + 8u * q;
+      store_masked(dst + t, x, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = kClosed;
-    if (open_token(mask, t)) {
-      const bool touched = (bits[u >> 5] >> (u & 31u)) & 1u;
-      y = __fmul_rn(touched ? __uint_as_float(word[u]) : load_elem(src + t), inv_t);
+    if (open_token(mask, open, s, t)) {
+      float x = load_elem(src + t);
+      if ((final[u >> 5] >> (u & 31u)) & 1u)
+        x = __uint_as_float(word[u]);
+      else if (word[u])
+        x = penalized(x, word[u]);
+      y = __fmul_rn(x, inv_t);
     }
     store_elem(dst + t, y);
   });
@@ -420,54 +576,57 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
 // Backward: a bit a token of the history, and the raw logits of groups that have one.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __grid_constant__ LogitsArgs a) {
-  __shared__ uint32_t bits[kWords];
-  __shared__ RowSettings row;
+  __shared__ uint32_t bits[kWords], open[kWords];
   const TOut* src = static_cast<const TOut*>(a.src);
   TIn* dst = static_cast<TIn*>(a.dst);
   Slice s = slice_of(a, src, dst);
+  const bool history = a.tokens && a.repetition;
+  const RowLoads loads = load_row(a, s.row, history);
   const TIn* raw = static_cast<const TIn*>(a.raw) + (a.raw ? s.row * a.raw_stride : 0u);
   if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
-  const uint32_t* mask = mask_of(a, s.row);
   Groups<TOut> g;
-  g.load(s, src, mask);
+  g.load(s, src);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
-  if (threadIdx.x == 0) read_row(a, s.row, a.tokens && a.repetition, row);
-  __syncthreads();
+  const uint32_t* mask = mask_of(a, loads);
+  copy_mask(mask, s, open);
+  const RowSettings row = settings_of(a, loads, history);
   if (row.history.end > row.history.begin) {
-    scan_tokens(a, s, a.tokens, row.history.begin, row.history.end, [&](bool in, uint32_t u, int64_t) {
-      if (in) atomicOr(bits + (u >> 5), 1u << (u & 31u));
-    });
     __syncthreads();
+    mark_history(a, s, row.history, bits);
   }
+  mask_ready();
+  __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
   Raw<TIn> x[kGroups];
+  uint32_t hit[kGroups];  // open tokens of the history
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads;
-    if (g.ok[r] && reinterpret_cast<const uint8_t*>(bits)[q + 1u]) load_group(raw + s.base + 8u * q, x[r]);
+    const uint32_t q = threadIdx.x + r * kThreads, t = s.base + 8u * q;
+    hit[r] = q < g.count ? reinterpret_cast<const uint8_t*>(bits)[q + 1u] : 0u;
+    if (hit[r] && mask) hit[r] &= mask_bits8(open, s, t);
+    if (hit[r]) load_group(raw + t, x[r]);
   }
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads;
+    const uint32_t q = threadIdx.x + r * kThreads, t = s.base + 8u * q;
     if (q < g.count) {
-      const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
       float d[8];
       values(g.x[r], d);
 #pragma unroll
       for (int k = 0; k < 8; ++k) d[k] = __fmul_rn(d[k], inv_t);
-      if (hit) {
+      if (hit[r]) {
         float v[8];
         values(x[r], v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = (hit >> k) & 1u ? __fmul_rn(d[k], v[k] > 0.0f ? inv_rep : rep) : d[k];
+        for (int k = 0; k < 8; ++k) d[k] = (hit[r] >> k) & 1u ? __fmul_rn(d[k], v[k] > 0.0f ? inv_rep : rep) : d[k];
       }
-      store_masked(dst + s.base + 8u * q, d, g.ok[r], 0.0f);
+      store_masked(dst + t, d, mask ? mask_bits8(open, s, t) : 0xFFu, 0.0f);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = 0.0f;
-    if (open_token(mask, t)) {
+    if (open_token(mask, open, s, t)) {
       y = __fmul_rn(load_elem(src + t), inv_t);
       if ((bits[u >> 5] >> (u & 31u)) & 1u) y = __fmul_rn(y, load_elem(raw + t) > 0.0f ? inv_rep : rep);
     }
@@ -475,34 +634,44 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __gr
   });
 }
 
+}  // namespace
+
 // Slices of a row: as few as possible, since every one reads the history, but
 // more where there are too few rows to give every SM two CTAs.
-void cut_rows(LogitsArgs& a, int sms) {
+void logits_cut(LogitsArgs& a, int sms) {
   uint32_t k = (a.vocab + kSliceMax - 1) / kSliceMax;
   while (a.rows * k < uint64_t(sms) * 2 && a.vocab / (2 * k) >= kSliceMin) k *= 2;
-  a.slices = k;
-  a.slice = ((a.vocab + k - 1) / k + 7u) & ~7u;
+  a.slice = ((a.vocab + k - 1) / k + 31u) & ~31u;
+  a.slices = (a.vocab + a.slice - 1) / a.slice;
 }
 
-template <typename K>
-cudaError_t launch_full(K kernel, const LogitsArgs& a, cudaStream_t stream) {
-  constexpr uint32_t kBytes = kPlaces * 6u;  // word, list
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBytes));
-  if (e != cudaSuccess) return e;
-  kernel<<<unsigned(a.rows * a.slices), kThreads, kBytes, stream>>>(a);
+// Worth it where the sorting moves no more than a part of what the rows are, and
+// every SM has several slices to gain from it.
+bool logits_sorts(const LogitsArgs& a, int sms) {
+  return a.slices >= 2 && a.slices <= kSortSlices && a.rows * a.slices >= uint64_t(sms) * 4 &&
+         uint64_t(a.ntokens) <= a.rows * a.vocab / 4 && a.ntokens > 0;
+}
+uint64_t logits_sort_blocks(const LogitsArgs& a) { return (uint64_t(a.ntokens) + kBlock - 1) / kBlock; }
+uint64_t logits_sort_entries(const LogitsArgs& a) { return logits_sort_blocks(a) * kBlock; }
+uint64_t logits_sort_offs(const LogitsArgs& a) { return logits_sort_blocks(a) * (a.slices + 2); }
+
+cudaError_t launch_logits_sort(const LogitsArgs& a, uint32_t* entries, uint16_t* offs, cudaStream_t stream) {
+  sort_kernel<<<unsigned(logits_sort_blocks(a)), 256, 0, stream>>>(a.tokens, uint64_t(a.ntokens), a.vocab, a.slice,
+                                                                   a.slices, entries, offs);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_logits_shape(LogitsArgs a, int in_type, int out_type, int sms, cudaStream_t stream) {
-  cut_rows(a, sms);
-  if (a.bias_tokens || (a.tokens && (a.presence || a.frequency))) {
-    if (in_type == PULSE_F32) return launch_full(shape_kernel<float, float>, a, stream);
-    if (out_type == PULSE_F32) return launch_full(shape_kernel<uint16_t, float>, a, stream);
-    return launch_full(shape_kernel<uint16_t, uint16_t>, a, stream);
-  }
+cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
   const unsigned grid = unsigned(a.rows * a.slices);
+  if (a.bias_tokens || (a.tokens && (a.presence || a.frequency))) {
+    if (in_type == PULSE_F32)
+      shape_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
+    else if (out_type == PULSE_F32)
+      shape_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
+    else
+      shape_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
   if (in_type == PULSE_F32)
     scale_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
   else if (out_type == PULSE_F32)
@@ -512,9 +681,7 @@ cudaError_t launch_logits_shape(LogitsArgs a, int in_type, int out_type, int sms
   return cudaGetLastError();
 }
 
-cudaError_t launch_logits_backward(LogitsArgs a, int in_type, int out_type, int sms,
-                                   cudaStream_t stream) {
-  cut_rows(a, sms);
+cudaError_t launch_logits_backward(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
   const unsigned grid = unsigned(a.rows * a.slices);
   if (in_type == PULSE_F32)
     backward_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);

@@ -425,6 +425,8 @@ struct LogitsArgs {
   int64_t mask_rows;
   uint64_t mask_stride;
   const int32_t* mask_row;
+  const uint32_t* sorted;       // tokens sorted by slice, or null
+  const uint16_t* sorted_offs;
   const void* src;          // logits (forward) or dout (backward)
   uint64_t src_stride;
   const void* raw;          // backward: raw logits
@@ -433,9 +435,17 @@ struct LogitsArgs {
   uint64_t dst_stride;
   uint32_t* error_word;
 };
-cudaError_t launch_logits_shape(LogitsArgs a, int in_type, int out_type, int sms,
-                                cudaStream_t stream);
-cudaError_t launch_logits_backward(LogitsArgs a, int in_type, int out_type, int sms,
+// Fills slices and slice (rows and vocab set); then whether the history is worth
+// sorting by slice, the room in words (entries) and half words (offs) it takes,
+// and the sorting itself.
+void logits_cut(LogitsArgs& a, int sms);
+bool logits_sorts(const LogitsArgs& a, int sms);
+uint64_t logits_sort_entries(const LogitsArgs& a);
+uint64_t logits_sort_offs(const LogitsArgs& a);
+cudaError_t launch_logits_sort(const LogitsArgs& a, uint32_t* entries, uint16_t* offs,
+                               cudaStream_t stream);
+cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream);
+cudaError_t launch_logits_backward(const LogitsArgs& a, int in_type, int out_type,
                                    cudaStream_t stream);
 
 int sm_count(int device);
