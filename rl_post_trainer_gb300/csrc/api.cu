@@ -1800,8 +1800,8 @@ bool logits_reserve(LogitsWorkspace& w, uint64_t entries, uint64_t offs, cudaStr
 // where `history` is read and the sorting pays.
 int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cudaStream_t stream,
                 LogitsArgs* a) {
-  // one CTA per slice of a row: the grid has to fit its 31 bits
-  if (rows > kMaxTiles / div_up(s.vocab, 1024)) return PULSE_ERR_RANGE;
+  // one CTA per slice of a row: rows fit the grid's second and third dimension
+  if (rows > (1ull << 30) || rows > kMaxTiles / div_up(s.vocab, 1024)) return PULSE_ERR_RANGE;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
   a->rows = rows;

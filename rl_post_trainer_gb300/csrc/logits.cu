@@ -31,6 +31,9 @@ constexpr uint32_t kSliceMin = 2048;
 constexpr uint32_t kSliceMax = 8u * kThreads * kGroups - 32u;
 constexpr uint32_t kWords = (kSliceMax + 8u + 31u) / 32u;  // of a bitmap of a slice's places
 constexpr uint32_t kPlaces = kWords * 32u;
+constexpr uint32_t kBlock = 2048;       // tokens that are sorted together
+constexpr uint32_t kSortSlices = 250;   // most slices that are sorted for
+constexpr unsigned kRowsY = 32768;      // rows of a grid's second dimension
 
 // A group is 8 elements of a row, 16 bytes of BF16 or 32 of FP32.
 __device__ __forceinline__ float load_elem(const float* p) { return *p; }
@@ -83,19 +86,22 @@ __device__ __forceinline__ uint32_t lead_of(const T* p) {
   return uint32_t(0u - uint32_t(reinterpret_cast<uintptr_t>(p) / sizeof(T))) & 7u;
 }
 
-struct Range {
-  int64_t begin, split, end;
+// A row's settings, read by the CTA's first warp. Ranges that do not fit their lists
+// are empty (and recorded).
+struct RowSettings {
+  const int32_t* tokens;   // the history; null where the tokens are sorted
+  uint32_t history, made;  // its length, and where its generated part starts
+  uint32_t block, from;    // sorted tokens: first block, and the history's place in it
+  uint32_t biased;         // length of the bias list
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  const uint32_t* mask;    // null: all tokens are open
+  float rep, inv_rep, pres, freq, inv_t;
 };
 
-// What a warp asks for of its row before anything else: a setting a lane, so that
-// one wait covers them all.
-struct RowLoads {
-  int64_t v8;
-  float v4;
-  int32_t mask_row;
-};
-__device__ __forceinline__ RowLoads load_row(const LogitsArgs& a, uint32_t row, bool history) {
-  const uint32_t lane = threadIdx.x & 31u;
+// A setting a lane, so that one wait covers them all.
+__device__ __forceinline__ void read_row(const LogitsArgs& a, uint32_t row, bool history, RowSettings& r) {
+  const uint32_t lane = threadIdx.x;
   const int64_t* p8 = nullptr;
   const float* p4 = nullptr;
   if (history) {
@@ -108,48 +114,29 @@ __device__ __forceinline__ RowLoads load_row(const LogitsArgs& a, uint32_t row, 
   if (lane == 6) p4 = a.temperature;
   if (lane == 7) p4 = a.presence;
   if (lane == 8) p4 = a.frequency;
-  RowLoads r;
-  r.v8 = p8 ? *p8 : 0;
-  r.v4 = p4 ? p4[row] : lane < 7 ? 1.0f : 0.0f;
-  r.mask_row = a.mask == nullptr ? -1 : a.mask_row ? a.mask_row[row] : int32_t(row);
-  return r;
-}
-
-// The row's settings. Ranges that do not fit their lists are empty (and recorded).
-struct RowSettings {
-  Range history, bias;
-  float rep, inv_rep, pres, freq, inv_t;
-};
-__device__ __forceinline__ RowSettings settings_of(const LogitsArgs& a, const RowLoads& l, bool history) {
-  auto i64 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, l.v8, k); };
-  auto f32 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, l.v4, k); };
-  RowSettings r;
-  r.history = Range{i64(0), i64(1), i64(2)};
-  r.bias = Range{i64(3), i64(3), i64(4)};
-  const bool h_ok = r.history.begin >= 0 && r.history.split >= r.history.begin &&
-                    r.history.end >= r.history.split && r.history.end <= a.ntokens;
-  const bool b_ok = r.bias.begin >= 0 && r.bias.end >= r.bias.begin && r.bias.end <= a.nbias;
-  if (!h_ok) r.history = Range{0, 0, 0};
-  if (!b_ok) r.bias = Range{0, 0, 0};
-  if (((history && !h_ok) || (a.bias_tokens && !b_ok)) && threadIdx.x == 0) record_error(a.error_word, kErrIndex);
-  const float t = f32(6);
-  r.rep = f32(5);
-  r.inv_rep = __frcp_rn(r.rep);
-  r.inv_t = t > 0.0f ? __frcp_rn(t) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
-  r.pres = f32(7);
-  r.freq = f32(8);
-  return r;
-}
-
-// The row's mask words, or null.
-__device__ __forceinline__ const uint32_t* mask_of(const LogitsArgs& a, const RowLoads& l) {
-  const int32_t m = l.mask_row;
-  if (m < 0) return nullptr;
-  if (m >= a.mask_rows) {
-    if (threadIdx.x == 0) record_error(a.error_word, kErrIndex);
-    return nullptr;
+  const int64_t v8 = p8 ? *p8 : 0;
+  const float v4 = p4 ? p4[row] : lane < 7 ? 1.0f : 0.0f;
+  const int64_t m = a.mask == nullptr ? -1 : a.mask_row ? int64_t(a.mask_row[row]) : int64_t(row);
+  auto i64 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, v8, k); };
+  const int64_t begin = i64(0), split = i64(1), end = i64(2), bias = i64(3), bias_end = i64(4);
+  const bool h_ok = begin >= 0 && split >= begin && end >= split && end <= a.ntokens && end - begin < (1ll << 31);
+  const bool b_ok = bias >= 0 && bias_end >= bias && bias_end <= a.nbias;
+  if (lane == 0) {
+    r.tokens = a.tokens + begin;
+    r.history = h_ok ? uint32_t(end - begin) : 0u;
+    r.made = uint32_t(split - begin);
+    r.block = uint32_t(begin / kBlock);
+    r.from = uint32_t(begin % kBlock);
+    r.biased = b_ok ? uint32_t(bias_end - bias) : 0u;
+    r.bias_tokens = a.bias_tokens + bias;
+    r.bias_values = a.bias_values + bias;
+    r.mask = m >= 0 && m < a.mask_rows ? a.mask + uint64_t(m) * a.mask_stride : nullptr;
+    if (!h_ok || !b_ok || (a.mask && m >= a.mask_rows)) record_error(a.error_word, kErrIndex);
   }
-  return a.mask + uint64_t(m) * a.mask_stride;
+  if (lane == 5) r.rep = v4, r.inv_rep = __frcp_rn(v4);
+  if (lane == 6) r.inv_t = v4 > 0.0f ? __frcp_rn(v4) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
+  if (lane == 7) r.pres = v4;
+  if (lane == 8) r.freq = v4;
 }
 
 // This CTA's part of a row: tokens [first, stop), groups from `base` on, up to 7
@@ -164,8 +151,8 @@ struct Slice {
 template <typename TSrc, typename TDst>
 __device__ __forceinline__ Slice slice_of(const LogitsArgs& a, const TSrc*& src, TDst*& dst) {
   Slice s;
-  s.row = blockIdx.x / a.slices;
-  s.index = blockIdx.x % a.slices;
+  s.row = blockIdx.z * kRowsY + blockIdx.y;
+  s.index = blockIdx.x;
   src += s.row * a.src_stride;
   dst += s.row * a.dst_stride;
   s.first = s.index * a.slice;  // a multiple of 32
@@ -187,44 +174,44 @@ struct Four {
 // an entry of the slice are left out: with a dozen slices a row that is most of
 // them. Tokens outside the vocabulary are recorded.
 template <typename F>
-__device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
-  const int32_t* p = a.tokens + h.begin;
+__device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s, const RowSettings& row, F f) {
+  const int32_t* p = row.tokens;
+  const uint32_t n = row.history, made = row.made;
   const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
   uint32_t bad = 0u;
-  auto four = [&](const int4& t, int64_t i, bool have) {
+  auto four = [&](const int4& t, uint32_t i, bool have) {
     const uint32_t v[4] = {uint32_t(t.x), uint32_t(t.y), uint32_t(t.z), uint32_t(t.w)};
     Four x;
     bool any = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x.in[k] = have && v[k] - s.first < len;
-      x.made[k] = i + k >= h.split;
+      x.made[k] = i + k >= made;
       x.u[k] = v[k] - s.first + off;
       bad |= have && v[k] >= a.vocab;
       any |= x.in[k];
     }
     if (__any_sync(0xFFFFFFFFu, any)) f(x);
   };
-  const int64_t n = h.end - h.begin;
-  const int64_t lead = min(n, int64_t((0u - uint32_t(reinterpret_cast<uintptr_t>(p) / 4u)) & 3u));
-  const int64_t quads = (n - lead) / 4, rest = lead + 4 * quads;
+  const uint32_t lead = min(n, (0u - uint32_t(reinterpret_cast<uintptr_t>(p) / 4u)) & 3u);
+  const uint32_t quads = (n - lead) / 4u, rest = lead + 4u * quads;
   const int4* quad = reinterpret_cast<const int4*>(p + lead);
   const int4 none = make_int4(-1, -1, -1, -1);
-  int64_t at = threadIdx.x;
+  uint32_t at = threadIdx.x;
   int4 next = at < quads ? __ldg(quad + at) : none;
-  for (int64_t q = threadIdx.x & ~31u; q < quads; q += kThreads, at += kThreads) {
+  for (uint32_t q = threadIdx.x & ~31u; q < quads; q += kThreads, at += kThreads) {
     const int4 t = next;
     next = at + kThreads < quads ? __ldg(quad + at + kThreads) : none;
-    four(t, h.begin + lead + 4 * at, at < quads);
+    four(t, lead + 4u * at, at < quads);
   }
   // up to 3 entries in front of the aligned ones and 3 behind, one a lane of the first warp
   if (threadIdx.x < 32u) {
-    const int64_t i = threadIdx.x < lead ? threadIdx.x : rest + (threadIdx.x - lead);
+    const uint32_t i = threadIdx.x < lead ? threadIdx.x : rest + (threadIdx.x - lead);
     const uint32_t t = i < n ? uint32_t(p[i]) : 0xFFFFFFFFu;
     bad |= i < n && t >= a.vocab;
     Four x{};
     x.in[0] = t - s.first < len;
-    x.made[0] = h.begin + i >= h.split;
+    x.made[0] = i >= made;
     x.u[0] = t - s.first + off;
     f(x);
   }
@@ -237,9 +224,6 @@ __device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s,
 // most of the work. With enough rows the token list is therefore sorted first:
 // block by block of kBlock tokens, the tokens of one slice side by side. A slice
 // then reads its own part of the blocks its history touches.
-constexpr uint32_t kBlock = 2048;
-constexpr uint32_t kSortSlices = 250;  // most slices that are sorted for
-
 // entries: place in the slice's vocabulary | position in the block << 16; offs:
 // for every block, where each slice's entries begin (slices + 2 words; the slice
 // past the last holds tokens outside the vocabulary).
@@ -251,7 +235,7 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   constexpr int kEach = kBlock / 256;
   const uint64_t base = uint64_t(blockIdx.x) * kBlock;
   count[threadIdx.x] = 0u;
-  uint32_t token[kEach], bucket[kEach], place[kEach];
+  uint32_t token[kEach], bucket[kEach], place[kEach] = {};
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const uint64_t i = base + threadIdx.x + 256 * k;
@@ -262,7 +246,10 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   for (int k = 0; k < kEach; ++k) {
     bucket[k] = token[k] < vocab ? token[k] / slice : slices;
     token[k] -= token[k] < vocab ? bucket[k] * slice : token[k];
-    place[k] = atomicAdd(count + bucket[k], 1u);
+    // frequent tokens have low numbers: most lanes may want the same count
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, bucket[k]), first = __ffs(same) - 1;
+    if ((threadIdx.x & 31u) == first) place[k] = atomicAdd(count + bucket[k], uint32_t(__popc(same)));
+    place[k] = __shfl_sync(0xFFFFFFFFu, place[k], int(first)) + __popc(same & lanemask_lt());
   }
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -288,23 +275,22 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
 
 // As scan_tokens, of sorted tokens.
 template <typename F>
-__device__ __forceinline__ void scan_sorted(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, row = a.slices + 2u;
-  const uint32_t b0 = uint32_t(h.begin / kBlock), blocks = uint32_t((h.end - 1) / kBlock) - b0 + 1u;
+__device__ __forceinline__ void scan_sorted(const LogitsArgs& a, const Slice& s, const RowSettings& row, F f) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, pitch = a.slices + 2u;
+  const uint32_t blocks = (row.from + row.history + kBlock - 1u) / kBlock;
   // warps share a block where there are fewer blocks than warps
   constexpr uint32_t kWarps = kThreads / 32;
-  uint32_t share = 1u;
-  while (share * 2u * blocks <= kWarps) share *= 2u;
+  const uint32_t share = blocks == 1u ? kWarps : blocks == 2u ? kWarps / 2u : blocks <= 4u ? kWarps / 4u : 1u;
   const uint32_t off = s.first - s.base + 8u, part = warp % share;
   uint32_t bad = 0u;
   for (uint32_t b = warp / share; b < blocks; b += kWarps / share) {
-    const int64_t base = int64_t(b0 + b) * kBlock;
-    const uint16_t* o = a.sorted_offs + uint64_t(b0 + b) * row + s.index;
-    const uint32_t* e = a.sorted + base;
+    const uint64_t block = uint64_t(row.block) + b;
+    const uint16_t* o = a.sorted_offs + block * pitch + s.index;
+    const uint32_t* e = a.sorted + block * kBlock;
     const uint32_t lo = o[0], hi = o[1];
     // the history's part of the block, and where its generated part starts
-    const uint32_t from = uint32_t(max(h.begin - base, int64_t(0))), to = uint32_t(min(h.end - base, int64_t(kBlock)));
-    const uint32_t made = uint32_t(min(max(h.split - base, int64_t(0)), int64_t(kBlock)));
+    const uint32_t from = b == 0u ? row.from : 0u, to = min(row.from + row.history - b * kBlock, kBlock);
+    const uint32_t split = row.from + row.made, made = split > b * kBlock ? split - b * kBlock : 0u;
     if (s.index == 0u && part == 0u)  // tokens outside the vocabulary, among the row's
       for (uint32_t i = o[a.slices] + lane; i < o[a.slices + 1u]; i += 32u) bad |= (e[i] >> 16) - from < to - from;
     for (uint32_t i = lo + part * 128u; i < hi; i += share * 128u) {
@@ -326,16 +312,17 @@ __device__ __forceinline__ void scan_sorted(const LogitsArgs& a, const Slice& s,
 }
 
 template <typename F>
-__device__ __forceinline__ void scan_history(const LogitsArgs& a, const Slice& s, const Range& h, F f) {
+__device__ __forceinline__ void scan_history(const LogitsArgs& a, const Slice& s, const RowSettings& row, F f) {
   if (a.sorted)
-    scan_sorted(a, s, h, f);
+    scan_sorted(a, s, row, f);
   else
-    scan_tokens(a, s, h, f);
+    scan_tokens(a, s, row, f);
 }
 
 // Sets the bits of the history.
-__device__ __forceinline__ void mark_history(const LogitsArgs& a, const Slice& s, const Range& h, uint32_t* bits) {
-  scan_history(a, s, h, [&](const Four& x) {
+__device__ __forceinline__ void mark_history(const LogitsArgs& a, const Slice& s, const RowSettings& row,
+                                             uint32_t* bits) {
+  scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (x.in[k]) atomicOr(bits + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
@@ -367,11 +354,10 @@ struct Groups {
 
   __device__ __forceinline__ void load(const Slice& s, const TSrc* src) {
     count = s.grouped && s.stop > s.base ? (s.stop - s.base) / 8u : 0u;
+    const TSrc* p = src + s.base + 8u * threadIdx.x;
 #pragma unroll
-    for (int r = 0; r < kGroups; ++r) {
-      const uint32_t q = threadIdx.x + r * kThreads;
-      if (q < count) load_group(src + s.base + 8u * q, x[r]);
-    }
+    for (int r = 0; r < kGroups; ++r)
+      if (threadIdx.x + r * kThreads < count) load_group(p + r * (8 * kThreads), x[r]);
   }
 };
 
@@ -409,24 +395,24 @@ constexpr float kClosed = -__builtin_huge_valf();
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_constant__ LogitsArgs a) {
   __shared__ uint32_t bits[kWords], open[kWords];
+  __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
-  const RowLoads loads = load_row(a, s.row, history);
+  if (s.row >= a.rows) return;
   Groups<TIn> g;
   g.load(s, src);
+  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
-  const uint32_t* mask = mask_of(a, loads);
+  __syncthreads();
+  const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  const RowSettings row = settings_of(a, loads, history);
-  if (row.history.end > row.history.begin) {
-    __syncthreads();
-    mark_history(a, s, row.history, bits);
-  }
+  if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
+  TOut* out = dst + s.base + 8u * threadIdx.x;
   auto seen = [&](float x) { return __fmul_rn(__fmul_rn(x, x > 0.0f ? inv_rep : rep), inv_t); };
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
@@ -442,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_
         for (int k = 0; k < 8; ++k) y[k] = (hit >> k) & 1u ? seen(x[k]) : y[k];
       }
       const uint32_t t = s.base + 8u * q;
-      store_masked(dst + t, y, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
+      store_masked(out + r * (8 * kThreads), y, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
@@ -463,38 +449,40 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
   // generated; where its bit in `final` is set, the logit with penalties and bias
   __shared__ __align__(16) uint32_t word[kPlaces];
   __shared__ uint32_t final[kWords], open[kWords];
+  __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && (a.repetition || a.presence || a.frequency);
-  const RowLoads loads = load_row(a, s.row, history);
+  if (s.row >= a.rows) return;
   Groups<TIn> g;
   g.load(s, src);
+  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
-  const uint32_t* mask = mask_of(a, loads);
-  copy_mask(mask, s, open);
-  const RowSettings row = settings_of(a, loads, history);
+  __syncthreads();
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const uint32_t* mask = row.mask;
+  copy_mask(mask, s, open);
   // Every warp reads the bias list backwards, 32 entries at a time, and serves the
   // places that are its own: the last entry of a token comes first, and its bit in
   // `final` turns the others away. The latest entries are asked for before the
   // history is read.
   constexpr int kAhead = 4;
-  const int64_t biased = row.bias.end - row.bias.begin;
+  const uint32_t biased = row.biased;
   uint32_t ahead[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
-    ahead[k] = int64_t(lane + 32 * k) < biased ? uint32_t(a.bias_tokens[row.bias.end - 1 - lane - 32 * k]) : 0xFFFFFFFFu;
-  __syncthreads();
+    ahead[k] = lane + 32u * k < biased ? uint32_t(row.bias_tokens[biased - 1u - lane - 32u * k]) : 0xFFFFFFFFu;
+  const float rep = row.rep, inv_rep = row.inv_rep, freq = row.freq, pres = row.pres, inv_t = row.inv_t;
   auto penalized = [&](float x, uint32_t st) {
     const uint32_t made = st & 0x7FFFFFFFu;
-    x = __fmul_rn(x, x > 0.0f ? row.inv_rep : row.rep);
-    return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(row.freq, float(made))), row.pres);
+    x = __fmul_rn(x, x > 0.0f ? inv_rep : rep);
+    return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(made))), pres);
   };
-  if (row.history.end > row.history.begin) {
-    scan_history(a, s, row.history, [&](const Four& x) {
+  if (row.history) {
+    scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (x.in[k]) {
@@ -504,13 +492,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
             atomicOr(word + x.u[k], 0x80000000u);
         }
     });
-    if (biased > 0) __syncthreads();
+    if (biased) __syncthreads();
   }
-  if (biased > 0) {
+  if (biased) {
     const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
     uint32_t bad = 0u;
-    auto serve = [&](uint32_t t, int64_t i) {  // a warp's lanes together; the lowest has the latest entry
-      bad |= i >= row.bias.begin && t >= a.vocab;
+    // a warp's lanes together, the entry `back` from the end; the lowest lane has the latest
+    auto serve = [&](uint32_t t, uint32_t back) {
+      bad |= back < biased && t >= a.vocab;
       const uint32_t u = t - s.first + off;
       const bool own = t - s.first < len && u * (kThreads / 32u) / kPlaces == warp;
       const uint32_t owners = __ballot_sync(0xFFFFFFFFu, own);
@@ -519,19 +508,18 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
       if (lane != uint32_t(__ffs(same) - 1)) return;
       if (atomicOr(final + (u >> 5), bit) & bit) return;
       const float x = load_elem(src + (s.base + u - 8u));
-      word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, a.bias_values[i]));
+      word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, row.bias_values[biased - 1u - back]));
     };
-    int64_t i = row.bias.end - 1 - lane;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k, i -= 32)
-      if (biased > 32 * k) serve(ahead[k], i);
-    for (int64_t left = biased - 32 * kAhead; left > 0; left -= 32, i -= 32)
-      serve(i >= row.bias.begin ? uint32_t(a.bias_tokens[i]) : 0xFFFFFFFFu, i);
+    for (int k = 0; k < kAhead; ++k)
+      if (biased > 32u * k) serve(ahead[k], lane + 32u * k);
+    for (uint32_t back = 32u * kAhead; back < biased; back += 32u)
+      serve(back + lane < biased ? uint32_t(row.bias_tokens[biased - 1u - back - lane]) : 0xFFFFFFFFu, back + lane);
     if (bad) record_error(a.error_word, kErrIndex);
   }
   mask_ready();
   __syncthreads();
-  const float inv_t = row.inv_t;
+  TOut* out = dst + s.base + 8u * threadIdx.x;
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
     const uint32_t q = threadIdx.x + r * kThreads;
@@ -555,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], inv_t);
       const uint32_t t = s.base + 8u * q;
-      store_masked(dst + t, x, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
+      store_masked(out + r * (8 * kThreads), x, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
@@ -577,26 +565,27 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __grid_constant__ LogitsArgs a) {
   __shared__ uint32_t bits[kWords], open[kWords];
+  __shared__ RowSettings row;
   const TOut* src = static_cast<const TOut*>(a.src);
   TIn* dst = static_cast<TIn*>(a.dst);
   Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
-  const RowLoads loads = load_row(a, s.row, history);
+  if (s.row >= a.rows) return;
   const TIn* raw = static_cast<const TIn*>(a.raw) + (a.raw ? s.row * a.raw_stride : 0u);
   if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
   Groups<TOut> g;
   g.load(s, src);
+  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
-  const uint32_t* mask = mask_of(a, loads);
+  __syncthreads();
+  const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  const RowSettings row = settings_of(a, loads, history);
-  if (row.history.end > row.history.begin) {
-    __syncthreads();
-    mark_history(a, s, row.history, bits);
-  }
+  if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
+  const TIn* near = raw + s.base + 8u * threadIdx.x;
+  TIn* out = dst + s.base + 8u * threadIdx.x;
   Raw<TIn> x[kGroups];
   uint32_t hit[kGroups];  // open tokens of the history
 #pragma unroll
@@ -604,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __gr
     const uint32_t q = threadIdx.x + r * kThreads, t = s.base + 8u * q;
     hit[r] = q < g.count ? reinterpret_cast<const uint8_t*>(bits)[q + 1u] : 0u;
     if (hit[r] && mask) hit[r] &= mask_bits8(open, s, t);
-    if (hit[r]) load_group(raw + t, x[r]);
+    if (hit[r]) load_group(near + r * (8 * kThreads), x[r]);
   }
 #pragma unroll
   for (int r = 0; r < kGroups; ++r) {
@@ -620,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __gr
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[k] = (hit[r] >> k) & 1u ? __fmul_rn(d[k], v[k] > 0.0f ? inv_rep : rep) : d[k];
       }
-      store_masked(dst + t, d, mask ? mask_bits8(open, s, t) : 0xFFu, 0.0f);
+      store_masked(out + r * (8 * kThreads), d, mask ? mask_bits8(open, s, t) : 0xFFu, 0.0f);
     }
   }
   each_single(s, g.count, [&](uint32_t t) {
@@ -632,6 +621,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __gr
     }
     store_elem(dst + t, y);
   });
+}
+
+dim3 grid_of(const LogitsArgs& a) {
+  return dim3(a.slices, unsigned(a.rows < kRowsY ? a.rows : kRowsY), unsigned((a.rows + kRowsY - 1) / kRowsY));
 }
 
 }  // namespace
@@ -662,7 +655,7 @@ cudaError_t launch_logits_sort(const LogitsArgs& a, uint32_t* entries, uint16_t*
 }
 
 cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
-  const unsigned grid = unsigned(a.rows * a.slices);
+  const dim3 grid = grid_of(a);
   if (a.bias_tokens || (a.tokens && (a.presence || a.frequency))) {
     if (in_type == PULSE_F32)
       shape_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
@@ -682,7 +675,7 @@ cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, 
 }
 
 cudaError_t launch_logits_backward(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
-  const unsigned grid = unsigned(a.rows * a.slices);
+  const dim3 grid = grid_of(a);
   if (in_type == PULSE_F32)
     backward_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
   else if (out_type == PULSE_F32)
