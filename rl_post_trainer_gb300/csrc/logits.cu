@@ -6,6 +6,8 @@
 // row's history and bias list meanwhile, keeps a bit for every token of its slice
 // that they name (and, where tokens are counted or biased, a word), and then works
 // off the slice from registers.
+#include <type_traits>
+
 #include "pulse.h"
 #include "pulse_device.cuh"
 #include "pulse_internal.h"
@@ -13,9 +15,6 @@
 namespace pulse {
 namespace {
 
-#ifndef PULSE_LOGITS_MIN
-#define PULSE_LOGITS_MIN 5
-#endif
 #ifndef PULSE_LOGITS_GROUPS
 #define PULSE_LOGITS_GROUPS 4
 #endif
@@ -23,12 +22,15 @@ namespace {
 #define PULSE_LOGITS_THREADS 256
 #endif
 constexpr int kThreads = PULSE_LOGITS_THREADS;
-constexpr int kMinCtas = PULSE_LOGITS_MIN;
+// CTAs per SM: as many as the registers of a slice's groups leave without spilling.
+template <typename TSrc>
+constexpr int kMinCtas = sizeof(TSrc) == 4 ? 4 : 5;
 // Groups of 8 elements a thread holds: its whole part of a slice, asked for
 // before the history is read.
 constexpr int kGroups = PULSE_LOGITS_GROUPS;
 constexpr uint32_t kSliceMin = 2048;
-constexpr uint32_t kSliceMax = 8u * kThreads * kGroups - 32u;
+constexpr uint32_t kRound = 8u * kThreads;  // tokens of a group a thread
+constexpr uint32_t kSliceMax = kRound * kGroups;
 constexpr uint32_t kWords = (kSliceMax + 8u + 31u) / 32u;  // of a bitmap of a slice's places
 constexpr uint32_t kPlaces = kWords * 32u;
 constexpr uint32_t kBlock = 2048;       // tokens that are sorted together
@@ -79,6 +81,15 @@ __device__ __forceinline__ void store_group(float* p, const float (&x)[8]) {
 __device__ __forceinline__ void store_group(uint16_t* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2_rn(x[0], x[1]), cvt_bf16x2_rn(x[2], x[3]),
                                             cvt_bf16x2_rn(x[4], x[5]), cvt_bf16x2_rn(x[6], x[7]));
+}
+// y = x * f, two products an instruction.
+__device__ __forceinline__ void scale8(const float (&x)[8], float f, float (&y)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; k += 2)
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(y[k]), "=f"(y[k + 1])
+        : "f"(x[k]), "f"(x[k + 1]), "f"(f));
 }
 // Elements from p to the next group boundary.
 template <typename T>
@@ -155,7 +166,7 @@ __device__ __forceinline__ Slice slice_of(const LogitsArgs& a, const TSrc*& src,
   s.index = blockIdx.x;
   src += s.row * a.src_stride;
   dst += s.row * a.dst_stride;
-  s.first = s.index * a.slice;  // a multiple of 32
+  s.first = s.index * a.slice;
   s.stop = min(s.first + a.slice, a.vocab);
   const uint32_t lead = lead_of(src);
   s.grouped = lead == lead_of(dst);
@@ -234,6 +245,8 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   __shared__ uint32_t begin[256];
   constexpr int kEach = kBlock / 256;
   const uint64_t base = uint64_t(blockIdx.x) * kBlock;
+  // the kernel that reads the entries may start with what it does before that
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   count[threadIdx.x] = 0u;
   uint32_t token[kEach], bucket[kEach], place[kEach] = {};
 #pragma unroll
@@ -272,6 +285,10 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   for (int k = 0; k < kEach; ++k)
     entries[base + begin[bucket[k]] + place[k]] = token[k] | ((threadIdx.x + 256u * k) << 16);
 }
+
+// Waits for the sorting in front of this kernel, if there is one. Everything that a
+// call writes is written after it.
+__device__ __forceinline__ void sorted_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // As scan_tokens, of sorted tokens.
 template <typename F>
@@ -319,13 +336,26 @@ __device__ __forceinline__ void scan_history(const LogitsArgs& a, const Slice& s
     scan_tokens(a, s, row, f);
 }
 
+// Shared-memory reductions under a predicate; a branch for each would cost more
+// than the rest of a scan.
+__device__ __forceinline__ void add_if(bool p, uint32_t* at, uint32_t x) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared::cta.add.u32 [%1], %2;\n\t}" ::"r"(uint32_t(p)),
+               "r"(smem_addr(at)), "r"(x)
+               : "memory");
+}
+__device__ __forceinline__ void or_if(bool p, uint32_t* at, uint32_t x) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared::cta.or.b32 [%1], %2;\n\t}" ::"r"(uint32_t(p)),
+               "r"(smem_addr(at)), "r"(x)
+               : "memory");
+}
+
 // Sets the bits of the history.
 __device__ __forceinline__ void mark_history(const LogitsArgs& a, const Slice& s, const RowSettings& row,
                                              uint32_t* bits) {
   scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (x.in[k]) atomicOr(bits + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
+      or_if(x.in[k], bits + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
   });
 }
 
@@ -357,9 +387,23 @@ struct Groups {
     const TSrc* p = src + s.base + 8u * threadIdx.x;
 #pragma unroll
     for (int r = 0; r < kGroups; ++r)
-      if (threadIdx.x + r * kThreads < count) load_group(p + r * (8 * kThreads), x[r]);
+      if (threadIdx.x + r * kThreads < count) load_group(p + r * kRound, x[r]);
   }
 };
+
+// Calls f(true type) for a slice without a mask whose threads all have a group in
+// every round but the last, else f(false type): f leaves out the checks.
+template <typename F>
+__device__ __forceinline__ void rounds(uint32_t groups, const uint32_t* mask, F f) {
+  if (mask == nullptr && groups >= (kGroups - 1) * uint32_t(kThreads))
+    f(std::true_type{});
+  else
+    f(std::false_type{});
+}
+template <bool PLAIN>
+__device__ __forceinline__ bool in_round(int r, uint32_t groups) {
+  return (PLAIN && r < kGroups - 1) || threadIdx.x + r * kThreads < groups;
+}
 
 template <typename TDst>
 __device__ __forceinline__ void store_masked(TDst* p, float (&y)[8], uint32_t ok, float masked) {
@@ -393,7 +437,7 @@ constexpr float kClosed = -__builtin_huge_valf();
 
 // Repetition penalty and temperature alone: a bit a token is all there is to keep.
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __grid_constant__ LogitsArgs a) {
   __shared__ uint32_t bits[kWords], open[kWords];
   __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
@@ -408,29 +452,30 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
+  sorted_ready();
   if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
   TOut* out = dst + s.base + 8u * threadIdx.x;
   auto seen = [&](float x) { return __fmul_rn(__fmul_rn(x, x > 0.0f ? inv_rep : rep), inv_t); };
+  rounds(g.count, mask, [&](auto plain) {
+    constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll
-  for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads;
-    if (q < g.count) {
+    for (int r = 0; r < kGroups; ++r) {
+      if (!in_round<kPlain>(r, g.count)) continue;
+      const uint32_t q = threadIdx.x + r * kThreads;
       const uint32_t hit = reinterpret_cast<const uint8_t*>(bits)[q + 1u];
       float x[8], y[8];
       values(g.x[r], x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = __fmul_rn(x[k], inv_t);
+      scale8(x, inv_t, y);
       if (hit) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = (hit >> k) & 1u ? seen(x[k]) : y[k];
       }
-      const uint32_t t = s.base + 8u * q;
-      store_masked(out + r * (8 * kThreads), y, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
+      store_masked(out + r * kRound, y, !kPlain && mask ? mask_bits8(open, s, s.base + 8u * q) : 0xFFu, kClosed);
     }
-  }
+  });
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = kClosed;
@@ -444,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) scale_kernel(const __grid_
 
 // Everything: tokens are counted and biased.
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __grid_constant__ LogitsArgs a) {
   // a word a place: bit 31 for a token of the prompt, below it the times it was
   // generated; where its bit in `final` is set, the logit with penalties and bias
   __shared__ __align__(16) uint32_t word[kPlaces];
@@ -481,16 +526,15 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
     x = __fmul_rn(x, x > 0.0f ? inv_rep : rep);
     return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(made))), pres);
   };
+  sorted_ready();
   if (row.history) {
     scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (x.in[k]) {
-          if (x.made[k])
-            atomicAdd(word + x.u[k], 1u);
-          else
-            atomicOr(word + x.u[k], 0x80000000u);
-        }
+      {
+        add_if(x.in[k] && x.made[k], word + x.u[k], 1u);
+        or_if(x.in[k] && !x.made[k], word + x.u[k], 0x80000000u);
+      }
     });
     if (biased) __syncthreads();
   }
@@ -520,10 +564,12 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
   mask_ready();
   __syncthreads();
   TOut* out = dst + s.base + 8u * threadIdx.x;
+  rounds(g.count, mask, [&](auto plain) {
+    constexpr bool kPlain = decltype(plain)::value;
 #pragma unroll
-  for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads;
-    if (q < g.count) {
+    for (int r = 0; r < kGroups; ++r) {
+      if (!in_round<kPlain>(r, g.count)) continue;
+      const uint32_t q = threadIdx.x + r * kThreads;
       float x[8];
       values(g.x[r], x);
       const uint32_t fin = reinterpret_cast<const uint8_t*>(final)[q + 1u];
@@ -540,12 +586,10 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
           for (int k = 0; k < 8; ++k) x[k] = (fin >> k) & 1u ? __uint_as_float(w[k]) : x[k];
         }
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], inv_t);
-      const uint32_t t = s.base + 8u * q;
-      store_masked(out + r * (8 * kThreads), x, mask ? mask_bits8(open, s, t) : 0xFFu, kClosed);
+      scale8(x, inv_t, x);
+      store_masked(out + r * kRound, x, !kPlain && mask ? mask_bits8(open, s, s.base + 8u * q) : 0xFFu, kClosed);
     }
-  }
+  });
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = kClosed;
@@ -563,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) shape_kernel(const __grid_
 
 // Backward: a bit a token of the history, and the raw logits of groups that have one.
 template <typename TIn, typename TOut>
-__global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(const __grid_constant__ LogitsArgs a) {
   __shared__ uint32_t bits[kWords], open[kWords];
   __shared__ RowSettings row;
   const TOut* src = static_cast<const TOut*>(a.src);
@@ -580,38 +624,40 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) backward_kernel(const __gr
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
+  sorted_ready();
   if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
   const TIn* near = raw + s.base + 8u * threadIdx.x;
   TIn* out = dst + s.base + 8u * threadIdx.x;
-  Raw<TIn> x[kGroups];
-  uint32_t hit[kGroups];  // open tokens of the history
+  rounds(g.count, mask, [&](auto plain) {
+    constexpr bool kPlain = decltype(plain)::value;
+    Raw<TIn> x[kGroups];
+    uint32_t hit[kGroups];  // open tokens of the history
 #pragma unroll
-  for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads, t = s.base + 8u * q;
-    hit[r] = q < g.count ? reinterpret_cast<const uint8_t*>(bits)[q + 1u] : 0u;
-    if (hit[r] && mask) hit[r] &= mask_bits8(open, s, t);
-    if (hit[r]) load_group(near + r * (8 * kThreads), x[r]);
-  }
+    for (int r = 0; r < kGroups; ++r) {
+      const uint32_t q = threadIdx.x + r * kThreads;
+      hit[r] = in_round<kPlain>(r, g.count) ? reinterpret_cast<const uint8_t*>(bits)[q + 1u] : 0u;
+      if (!kPlain && hit[r] && mask) hit[r] &= mask_bits8(open, s, s.base + 8u * q);
+      if (hit[r]) load_group(near + r * kRound, x[r]);
+    }
 #pragma unroll
-  for (int r = 0; r < kGroups; ++r) {
-    const uint32_t q = threadIdx.x + r * kThreads, t = s.base + 8u * q;
-    if (q < g.count) {
+    for (int r = 0; r < kGroups; ++r) {
+      if (!in_round<kPlain>(r, g.count)) continue;
       float d[8];
       values(g.x[r], d);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = __fmul_rn(d[k], inv_t);
+      scale8(d, inv_t, d);
       if (hit[r]) {
         float v[8];
         values(x[r], v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[k] = (hit[r] >> k) & 1u ? __fmul_rn(d[k], v[k] > 0.0f ? inv_rep : rep) : d[k];
       }
-      store_masked(out + r * (8 * kThreads), d, mask ? mask_bits8(open, s, t) : 0xFFu, 0.0f);
+      const uint32_t t = s.base + 8u * (threadIdx.x + r * kThreads);
+      store_masked(out + r * kRound, d, !kPlain && mask ? mask_bits8(open, s, t) : 0xFFu, 0.0f);
     }
-  }
+  });
   each_single(s, g.count, [&](uint32_t t) {
     const uint32_t u = t - s.base + 8u;
     float y = 0.0f;
@@ -627,14 +673,29 @@ dim3 grid_of(const LogitsArgs& a) {
   return dim3(a.slices, unsigned(a.rows < kRowsY ? a.rows : kRowsY), unsigned((a.rows + kRowsY - 1) / kRowsY));
 }
 
+// Behind the sorting of its tokens the kernel may start early (sorted_ready).
+template <typename K>
+cudaError_t launch(K kernel, const LogitsArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid_of(a);
+  c.blockDim = dim3(kThreads);
+  c.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = a.sorted ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 }  // namespace
 
 // Slices of a row: as few as possible, since every one reads the history, but
 // more where there are too few rows to give every SM two CTAs.
 void logits_cut(LogitsArgs& a, int sms) {
-  uint32_t k = (a.vocab + kSliceMax - 1) / kSliceMax;
-  while (a.rows * k < uint64_t(sms) * 2 && a.vocab / (2 * k) >= kSliceMin) k *= 2;
-  a.slice = ((a.vocab + k - 1) / k + 31u) & ~31u;
+  uint32_t k = (a.vocab + kSliceMax - 1) / kSliceMax, unit = kRound;
+  while (a.rows * k < uint64_t(sms) * 2 && a.vocab / (2 * k) >= kSliceMin) k *= 2, unit = 32u;
+  a.slice = ((a.vocab + k - 1) / k + unit - 1) / unit * unit;
   a.slices = (a.vocab + a.slice - 1) / a.slice;
 }
 
@@ -655,34 +716,20 @@ cudaError_t launch_logits_sort(const LogitsArgs& a, uint32_t* entries, uint16_t*
 }
 
 cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
-  const dim3 grid = grid_of(a);
   if (a.bias_tokens || (a.tokens && (a.presence || a.frequency))) {
-    if (in_type == PULSE_F32)
-      shape_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
-    else if (out_type == PULSE_F32)
-      shape_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
-    else
-      shape_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (in_type == PULSE_F32) return launch(shape_kernel<float, float>, a, stream);
+    if (out_type == PULSE_F32) return launch(shape_kernel<uint16_t, float>, a, stream);
+    return launch(shape_kernel<uint16_t, uint16_t>, a, stream);
   }
-  if (in_type == PULSE_F32)
-    scale_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
-  else if (out_type == PULSE_F32)
-    scale_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
-  else
-    scale_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (in_type == PULSE_F32) return launch(scale_kernel<float, float>, a, stream);
+  if (out_type == PULSE_F32) return launch(scale_kernel<uint16_t, float>, a, stream);
+  return launch(scale_kernel<uint16_t, uint16_t>, a, stream);
 }
 
 cudaError_t launch_logits_backward(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {
-  const dim3 grid = grid_of(a);
-  if (in_type == PULSE_F32)
-    backward_kernel<float, float><<<grid, kThreads, 0, stream>>>(a);
-  else if (out_type == PULSE_F32)
-    backward_kernel<uint16_t, float><<<grid, kThreads, 0, stream>>>(a);
-  else
-    backward_kernel<uint16_t, uint16_t><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (in_type == PULSE_F32) return launch(backward_kernel<float, float>, a, stream);
+  if (out_type == PULSE_F32) return launch(backward_kernel<uint16_t, float>, a, stream);
+  return launch(backward_kernel<uint16_t, uint16_t>, a, stream);
 }
 
 }  // namespace pulse
