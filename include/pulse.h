@@ -744,7 +744,7 @@ int pulse_encode_noalloc(const float *master_f32, uint16_t *prev_bf16, uint64_t 
  *   d = lr * lr_scale * weight_decay
  * m and v are reproducible bit for bit (no fused multiply-add); the quotient
  * and the square root in w may be off by a few units in the last place of the
- * update. A grad_scale that is not finite leaves w, m and v as they are (the
+ * update, and a v below 2^-126 counts as 0 under the root. A grad_scale that is not finite leaves w, m and v as they are (the
  * step of a step's non-finite gradients is skipped without a host round trip).
  *
  * 8-bit moments. Blocks of 256 consecutive elements of a tensor (the last may
@@ -821,9 +821,10 @@ int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
  * pulse_grad_norm_multi -- norm_out[0] = sqrt(sum of the squares of every
  * gradient of the plan); clip_out[0] = min(1, max_norm / (norm + 1e-6)), or NaN
  * where the norm is not finite, so that a step given clip_out as grad_scale is
- * skipped. Squares are summed in FP32 over at most 64 elements and in FP64 from
- * there on, in an order that depends on sizes alone: the same gradients give
- * the same bits. Gradients above about 1e18 overflow to an infinite norm.
+ * skipped. Squares are summed in FP32 over 16 elements and in pairs of FP32
+ * numbers (about 48 bits) from there on, in an order that depends on the sizes
+ * and the device alone: the same gradients give the same bits. A sum of squares
+ * past FP32's range (gradients above about 1e18) gives a norm that is not finite.
  *   norm_out, clip_out  device, one float each; clip_out may be NULL
  *   max_norm            >= 0 (infinity: never clips)
  */
@@ -848,12 +849,13 @@ int pulse_adam_export_multi(pulse_adam_plan *plan, cudaStream_t stream);
  * The weights that a patch updates produce the logits; nothing on the pages
  * describes this step.
  *
- * For row r and token t, in FP32, one operation after the other:
+ * For row r and token t, in FP32, one operation after the other; quotients are
+ * products with the divisor's rounded reciprocal:
  *   x = logits[r][t]
  *   t in the row's history:      x = x > 0 ? x / repetition[r] : x * repetition[r]
- *   c = times t was generated:   x = x - frequency[r] * c;  if c > 0: x = x - presence[r]
+ *   c = times t was generated:   if c > 0: x = x - frequency[r] * c - presence[r]
  *   t in the row's bias list:    x = x + its value (of a token listed twice, the last entry's)
- *   y = x * (1 / temperature[r]) (a temperature that is not above 0: y = x)
+ *   y = x / temperature[r] (a temperature that is not above 0: y = x)
  *   mask bit of t clear:         y = -infinity, whatever x was
  * out[r][t] = y, rounded to the output type. Backward, with d the gradient of y:
  *   dx = d / temperature[r];  t in the history: dx = logits[r][t] > 0 ? dx / repetition[r] : dx * repetition[r]
@@ -861,9 +863,17 @@ int pulse_adam_export_multi(pulse_adam_plan *plan, cudaStream_t stream);
  * A row whose mask allows nothing is all -infinity and has a zero gradient.
  *
  * Every pointer may be NULL: the step it belongs to is then left out. History
- * of row r: tokens[begin[r] .. end[r]), generated from split[r] on (split NULL:
- * all of it generated). Rows may share or overlap ranges, as the positions of
- * one training sequence do. Nothing is kept between calls.
+ * of row r: tokens[begin[r] .. end[r]), fewer than 2^31, generated from split[r]
+ * on (split NULL: all of it generated). Rows may share or overlap ranges, as the
+ * positions of one training sequence do.
+ *
+ * With many rows a call first sorts the tokens by where in the vocabulary they
+ * fall, into a library workspace per (device, stream) of about 4 bytes a token,
+ * allocated on first use and grown on demand (growth synchronises `stream`).
+ * Nothing of it is kept for the next call. A call that is being captured into a
+ * graph, and one without room, works on the tokens as they are. Errors of a stream
+ * that made its first call in a capture are reported by pulse_get_error of every
+ * stream.
  * ---------------------------------------------------------------------- */
 typedef struct pulse_logits_shaping {
   uint64_t vocab;            /* columns, in [1, 2^31) */
@@ -892,7 +902,9 @@ typedef struct pulse_logits_shaping {
  * logits itself (same type and stride); any other overlap is refused.
  * A token number outside [0, vocab), a range outside its list or a mask row
  * past mask_rows is left out and recorded as PULSE_ERR_INDEX for
- * pulse_get_error(stream). rows == 0 launches nothing.
+ * pulse_get_error(stream). rows == 0 launches nothing. Errors: PULSE_ERR_INVALID,
+ * PULSE_ERR_RANGE (rows > 2^30, or too many rows for the vocabulary),
+ * PULSE_ERR_NOMEM, PULSE_ERR_CUDA.
  */
 int pulse_logits_shape(const pulse_logits_shaping *shaping, uint64_t rows, const void *logits,
                        uint64_t stride, int in_type, void *out, uint64_t out_stride, int out_type,

@@ -273,9 +273,26 @@ struct Block8 {
   uint2 m, v;
 };
 
-template <bool BF16>
+// ALIGNED: weights and gradients can be read in groups of 8 as well as the codes.
+template <bool BF16, bool ALIGNED>
 __device__ __forceinline__ void load_block8(Block8<BF16>& b, const Adam8Ptrs& p, uint64_t block) {
   const uint64_t i = block * kAdamBlock + (threadIdx.x & 31u) * 8u;
+  b.m = ld_u2_no_l1(p.m + i);
+  b.v = ld_u2_no_l1(p.v + i);
+  if (!ALIGNED) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b.w.x[k] = p.w[i + k];
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 4 : 8); ++k) {
+      if (BF16) {
+        const uint16_t* g = static_cast<const uint16_t*>(p.g) + i + 2 * k;
+        b.g[k] = __uint_as_float(g[0] | uint32_t(g[1]) << 16);
+      } else {
+        b.g[k] = static_cast<const float*>(p.g)[i + k];
+      }
+    }
+    return;
+  }
   b.w = ld_f8(p.w + i);
   if (BF16) {
     const uint4 u = ld_stream_u4_ro(static_cast<const uint16_t*>(p.g) + i);
@@ -286,8 +303,6 @@ __device__ __forceinline__ void load_block8(Block8<BF16>& b, const Adam8Ptrs& p,
 #pragma unroll
     for (int k = 0; k < 8; ++k) b.g[BF16 ? 0 : k] = u.x[k];
   }
-  b.m = ld_u2_no_l1(p.m + i);
-  b.v = ld_u2_no_l1(p.v + i);
 }
 
 template <bool BF16>
@@ -305,7 +320,7 @@ __device__ __forceinline__ uint64_t grad_pair(const Block8<BF16>& b, int pair) {
 // kept short: zero codes, zero second moments, and exponents at the ends of
 // their range (infinities and NaN among them) take the general conversions,
 // decided once per warp.
-template <bool BF16>
+template <bool BF16, bool ALIGNED>
 __device__ __forceinline__ void adam8_block_full(const AdamLaunch& a, const Adam8Ptrs& p,
                                                  uint64_t block, uint32_t key, Block8<BF16>& b,
                                                  uint32_t& em, uint32_t& ev) {
@@ -358,7 +373,12 @@ __device__ __forceinline__ void adam8_block_full(const AdamLaunch& a, const Adam
     const uint64_t u = fma2(w, pack2(p.decay, p.decay), mul2(q, pack2(p.alpha, p.alpha)));
     unpack2(fma2(u, pack2(-1.0f, -1.0f), w), b.w.x[k], b.w.x[k + 1]);
   }
-  st_f8(p.w + i, b.w);
+  if (ALIGNED) {
+    st_f8(p.w + i, b.w);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p.w[i + k] = b.w.x[k];
+  }
   const uint32_t me = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)) >> 23;
   const uint32_t ve = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vx)) >> 23;
   const uint32_t me2 = min(max(me, 15u), 253u), ve2 = min(max(ve, 31u), 253u);
@@ -404,12 +424,11 @@ __device__ __forceinline__ void adam8_block_full(const AdamLaunch& a, const Adam
   ev = ve == 255u ? 0xFFu : ve2;
 }
 
-#ifndef PULSE_ADAM8_MIN_BLOCKS
-#define PULSE_ADAM8_MIN_BLOCKS 4
-#endif
+// CTAs per SM: 64 registers a thread. With 5 (48, some spilled) or 3 the step is slower.
+constexpr int kAdam8Ctas = 4;
 
 // `count` whole blocks of one warp, from `block` on.
-template <bool BF16>
+template <bool BF16, bool ALIGNED>
 __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptrs& p, uint64_t block,
                                              uint32_t count, uint64_t block_begin) {
   // A block's key and exponents are the same for the whole warp: each lane makes
@@ -424,13 +443,13 @@ __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptr
   }
   auto one = [&](uint32_t k, Block8<BF16>& y) {
     uint32_t em = __shfl_sync(0xFFFFFFFFu, ems, int(k)), ev = __shfl_sync(0xFFFFFFFFu, evs, int(k));
-    adam8_block_full(a, p, block + k, __shfl_sync(0xFFFFFFFFu, keys, int(k)), y, em, ev);
+    adam8_block_full<BF16, ALIGNED>(a, p, block + k, __shfl_sync(0xFFFFFFFFu, keys, int(k)), y, em, ev);
     if (lane == k) ems = em, evs = ev;
   };
 #pragma unroll 1
   for (uint32_t k = 0; k < count; ++k) {
     Block8<BF16> y;
-    load_block8(y, p, block + k);
+    load_block8<BF16, ALIGNED>(y, p, block + k);
     one(k, y);
   }
   if (lane < count) {
@@ -439,8 +458,11 @@ __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptr
   }
 }
 
-__global__ void __launch_bounds__(kAdamThreads, PULSE_ADAM8_MIN_BLOCKS)
-    adam8_kernel(const __grid_constant__ AdamLaunch a) {
+// MIXED: some tensor of the plan is not aligned for groups throughout. The kernel
+// for aligned plans keeps its registers without the code for the others (the
+// 1.5B-parameter step 3.41 ms against 3.48 with both in one).
+template <bool MIXED>
+__global__ void __launch_bounds__(kAdamThreads, kAdam8Ctas) adam8_kernel(const __grid_constant__ AdamLaunch a) {
   const AdamTensorDesc* const desc = a.tensors + a.tile_tensor[blockIdx.x];
   const AdamTensorDesc d = *desc;
   Adam8Ptrs p{d.w, d.g, static_cast<uint8_t*>(d.m), static_cast<uint8_t*>(d.v), d.m_exp, d.v_exp,
@@ -452,14 +474,16 @@ __global__ void __launch_bounds__(kAdamThreads, PULSE_ADAM8_MIN_BLOCKS)
   const uint32_t per_warp = a.tile / kAdamBlock / (kAdamThreads / 32);
   const uint64_t first = (blockIdx.x - d.tile_begin) * (a.tile / kAdamBlock) +
                          (threadIdx.x >> 5) * per_warp;
-  const uint64_t whole = lead == 0u ? n / kAdamBlock : 0u;  // blocks that take the short way
+  const uint64_t whole = MIXED && lead == kAdamNoGroups ? 0u : n / kAdamBlock;  // blocks that take the short way
   uint32_t done = 0;
   if (first < whole) {
     done = uint32_t(min(whole - first, uint64_t(per_warp)));
-    if (bf16)
-      adam8_blocks<true>(a, p, first, done, block_begin);
+    if (!MIXED || lead == 0u)
+      bf16 ? adam8_blocks<true, true>(a, p, first, done, block_begin)
+           : adam8_blocks<false, true>(a, p, first, done, block_begin);
     else
-      adam8_blocks<false>(a, p, first, done, block_begin);
+      bf16 ? adam8_blocks<true, false>(a, p, first, done, block_begin)
+           : adam8_blocks<false, false>(a, p, first, done, block_begin);
   }
   for (; done < per_warp && (first + done) * kAdamBlock < n; ++done)
     adam8_block_any(a, desc, p.scale, p.alpha, p.decay, first + done);
@@ -660,7 +684,10 @@ cudaError_t launch_adam32(const AdamLaunch& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_adam8(const AdamLaunch& a, cudaStream_t stream) {
-  adam8_kernel<<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
+  if (a.mixed)
+    adam8_kernel<true><<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
+  else
+    adam8_kernel<false><<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -108,6 +108,9 @@ int workspace_take_error(Workspace& ws, cudaStream_t stream) {
 std::mutex g_ws_mu;
 std::map<std::pair<int, uintptr_t>, Workspace*> g_ws;
 
+// Counter words of the library itself, per device (logits_capture_counters); never freed.
+std::map<int, Workspace> g_capture_ws;
+
 Workspace* stream_workspace(int device, cudaStream_t stream) {
   auto key = std::make_pair(device, reinterpret_cast<uintptr_t>(stream));
   auto it = g_ws.find(key);
@@ -399,6 +402,7 @@ struct pulse_adam_plan {
   uint32_t tile = 0;                  // elements per tile
   uint64_t total_tiles = 0;
   bool can_step = false;
+  bool mixed = false;                 // some tensor's lead is not 0
   std::vector<AdamTensorDesc> host_desc;
   AdamTensorDesc* desc = nullptr;     // device copy
   AdamTensorDesc* staging = nullptr;  // pinned copy that pulse_adam_plan_set_grads sends
@@ -508,7 +512,9 @@ int pulse_get_error(cudaStream_t stream) {
   auto ct = g_cmp_ws.find(key);
   const int e1 = take_error_pair(it == g_ws.end() ? nullptr : it->second,
                                  mt == g_mx_ws.end() ? nullptr : mt->second, stream);
-  const int e2 = take_error_pair(ct == g_cmp_ws.end() ? nullptr : &ct->second->ws, nullptr, stream);
+  auto gt = g_capture_ws.find(device);
+  const int e2 = take_error_pair(ct == g_cmp_ws.end() ? nullptr : &ct->second->ws,
+                                 gt == g_capture_ws.end() ? nullptr : &gt->second, stream);
   if (e1 == PULSE_ERR_CUDA || e2 == PULSE_ERR_CUDA) return PULSE_ERR_CUDA;
   if (e1 == PULSE_ERR_TIMEOUT || e2 == PULSE_ERR_TIMEOUT) return PULSE_ERR_TIMEOUT;
   return e1 != PULSE_OK ? e1 : e2;
@@ -1531,12 +1537,18 @@ uint32_t lead_of(const void* p, uint32_t elem) {
 
 uint32_t adam_lead(const AdamTensorDesc& d, int state_bits) {
   const uint32_t lead = lead_of(d.w, 4);
-  bool same = lead_of(d.g, d.grad_bf16 ? 2 : 4) == lead;
-  if (state_bits == 8)
-    same = same && lead == 0 && aligned(d.m, 8) && aligned(d.v, 8);
-  else
-    same = same && lead_of(d.m, 4) == lead && lead_of(d.v, 4) == lead;
-  return same ? lead : kAdamNoGroups;
+  const bool same = lead_of(d.g, d.grad_bf16 ? 2 : 4) == lead;
+  if (state_bits == 8) {
+    if (!aligned(d.m, 8) || !aligned(d.v, 8)) return kAdamNoGroups;
+    return same && lead == 0 ? 0u : kAdamCodeGroups;
+  }
+  return same && lead_of(d.m, 4) == lead && lead_of(d.v, 4) == lead ? lead : kAdamNoGroups;
+}
+
+bool adam_mixed(const std::vector<AdamTensorDesc>& desc) {
+  for (const AdamTensorDesc& d : desc)
+    if (d.lead != 0 && d.n > 0) return true;
+  return false;
 }
 
 // 8-bit moments: a warp takes tile / 2048 blocks one after the other. Four of
@@ -1632,6 +1644,7 @@ int pulse_adam_plan_create(const pulse_adam_tensor* tensors, int ntensors, int s
         p->can_step = p->can_step && t.master && t.m && t.v &&
                       (state_bits == 32 || (t.m_exp && t.v_exp));
     }
+    p->mixed = adam_mixed(p->host_desc);
     st = adam_plan_tables(p, tile_tensor);
   } catch (const std::bad_alloc&) {
     st = PULSE_ERR_NOMEM;
@@ -1666,6 +1679,7 @@ int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, c
     d.g = grads[i];
     d.lead = adam_lead(d, plan->state_bits);
   }
+  plan->mixed = adam_mixed(plan->host_desc);
   // the copy before this one has left the pinned buffer
   if (cudaEventSynchronize(plan->staged) != cudaSuccess) return PULSE_ERR_CUDA;
   const size_t bytes = sizeof(AdamTensorDesc) * plan->host_desc.size();
@@ -1697,6 +1711,7 @@ int pulse_adam_step_multi(pulse_adam_plan* plan, const pulse_adam_hyper* h, cons
   a.tile_tensor = plan->tile_tensor;
   a.total_tiles = plan->total_tiles;
   a.tile = plan->tile;
+  a.mixed = plan->mixed;
   a.grad_scale = grad_scale;
   a.alpha = float(h->lr / (1.0 - std::pow(h->beta1, t)));
   a.lr = float(h->lr);
@@ -1772,13 +1787,15 @@ struct LogitsWorkspace {
 };
 std::map<std::pair<int, uintptr_t>, LogitsWorkspace*> g_logits_ws;
 
+bool stream_captured(cudaStream_t stream) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
+}
+
 // Room for a call's sorted histories; growth synchronises `stream`. Returns false
-// where there is none (no memory, or the stream is being captured): the call then
-// works on the unsorted tokens.
+// where there is no memory for it: the call then works on the unsorted tokens.
 bool logits_reserve(LogitsWorkspace& w, uint64_t entries, uint64_t offs, cudaStream_t stream) {
   if (entries <= w.entry_cap && offs <= w.offs_cap) return true;
-  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return false;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return false;
   if (w.entries) cudaFree(w.entries);
   if (w.offs) cudaFree(w.offs);
@@ -1828,10 +1845,16 @@ int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cuda
   std::lock_guard<std::mutex> lock(g_ws_mu);
   Workspace* ws = stream_workspace(device, stream);
   if (ws == nullptr) return PULSE_ERR_NOMEM;
+  if (ws->counters == nullptr && stream_captured(stream)) {
+    ws = &g_capture_ws[device];
+    if (ws->counters == nullptr) ws->counters = logits_capture_counters();
+    if (ws->counters == nullptr) return PULSE_ERR_CUDA;
+  }
   const int st = workspace_reserve(*ws, 0, stream);
   if (st != PULSE_OK) return st;
   a->error_word = ws->counters + 2;
-  if (!history || !logits_sorts(*a, sms)) return PULSE_OK;
+  // a captured call may be replayed when the workspace has grown or is in use
+  if (!history || !logits_sorts(*a, sms) || stream_captured(stream)) return PULSE_OK;
   LogitsWorkspace*& lw = g_logits_ws[std::make_pair(device, reinterpret_cast<uintptr_t>(stream))];
   if (lw == nullptr) lw = new (std::nothrow) LogitsWorkspace();
   if (lw == nullptr) return PULSE_ERR_NOMEM;

@@ -690,6 +690,15 @@ cudaError_t launch(K kernel, const LogitsArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
+// Counter words for calls on a stream that has none and is being captured, where
+// nothing can be allocated.
+__device__ uint32_t g_capture_counters[64];
+
+uint32_t* logits_capture_counters() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_capture_counters) == cudaSuccess ? static_cast<uint32_t*>(p) : nullptr;
+}
+
 // Slices of a row: as few as possible, since every one reads the history, but
 // more where there are too few rows to give every SM two CTAs.
 void logits_cut(LogitsArgs& a, int sms) {

@@ -369,17 +369,18 @@ struct alignas(16) AdamTensorDesc {  // read in 16-byte pieces
   uint32_t grad_bf16;
   // Elements before the first one from which every buffer can be accessed in
   // groups of 8 (32 bytes of FP32, 16 of BF16, 8 codes); kAdamNoGroups where no
-  // common one exists. 8-bit moments: 0 or kAdamNoGroups, since a group must
-  // not straddle two blocks.
+  // common one exists. 8-bit moments: 0 (a group must not straddle two blocks),
+  // or kAdamCodeGroups where the codes have groups, weights or gradients not.
   uint32_t lead;
 };
-constexpr uint32_t kAdamNoGroups = 8;
+constexpr uint32_t kAdamNoGroups = 8, kAdamCodeGroups = 9;
 
 struct AdamLaunch {
   const AdamTensorDesc* tensors;  // device
   const uint32_t* tile_tensor;    // device: tensor of each tile
   uint64_t total_tiles;
   uint32_t tile;                  // elements per tile
+  bool mixed;                     // some tensor's lead is not 0
   const float* grad_scale;        // device, or null
   float alpha;                    // lr / (1 - beta1^step)
   float lr;
@@ -439,6 +440,7 @@ struct LogitsArgs {
 // sorting by slice, the room in words (entries) and half words (offs) it takes,
 // and the sorting itself.
 void logits_cut(LogitsArgs& a, int sms);
+uint32_t* logits_capture_counters();  // of the current device; null on an error
 bool logits_sorts(const LogitsArgs& a, int sms);
 uint64_t logits_sort_entries(const LogitsArgs& a);
 uint64_t logits_sort_offs(const LogitsArgs& a);

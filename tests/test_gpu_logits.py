@@ -320,6 +320,90 @@ def test_bad_indices_are_left_out_and_recorded():
     assert torch.equal(y[:2], x[:2]) and (y[2] == -float("inf")).all()
 
 
+# With many CTAs' worth of rows the tokens are sorted by vocabulary slice first, in blocks of 2048
+# positions; the vocabularies here give two slices and more.
+@pytest.mark.parametrize("tin,tout", PAIRS)
+@pytest.mark.parametrize("vocab", [16384, 20011, 24600])
+def test_many_rows(tin, tout, vocab):
+    _cuda()
+    rows = 420
+    check(settings(rows, vocab, history=60, seed=vocab, masks=7), rows, vocab, tin, tout)
+
+
+@pytest.mark.parametrize("history", [1, 2047, 2048, 2049, 9000])
+def test_many_rows_at_the_edges_of_sorted_blocks(history):
+    """Histories that begin, split and end around block boundaries, and rows that share them."""
+    _cuda()
+    rows, vocab = 610, 8500
+    g = np.random.default_rng(history)
+    total = history + 4200
+    s = settings(rows, vocab, seed=21, bias=3)
+    s["tokens"] = np.minimum(np.exp(g.random(total) * np.log(vocab)).astype(np.int64) - 1, vocab - 1).clip(0).astype(np.int32)
+    s["begin"] = g.integers(0, 4200, rows)
+    s["begin"][:6] = [0, 2047, 2048, 2049, 4095, 4096]
+    s["end"] = s["begin"] + history
+    s["end"][7] = s["begin"][7]
+    s["split"] = s["begin"] + (np.arange(rows) * 37) % (history + 1)
+    s["split"][7] = s["begin"][7]
+    check(s, rows, vocab, F32, F32)
+
+
+def test_many_rows_of_one_sequence():
+    _cuda()
+    rows, vocab = 2300, 8300
+    s = settings(rows, vocab, seed=22, bias=0)
+    for k in ("bias_tokens", "bias_values", "bias_begin"):
+        s[k] = None
+    s["tokens"] = np.random.default_rng(1).integers(0, vocab, rows).astype(np.int32)
+    s["begin"] = np.zeros(rows, np.int64)
+    s["end"] = np.arange(rows)
+    s["split"] = np.minimum(s["end"], 40)
+    check(s, rows, vocab, BF16, BF16)
+
+
+def test_many_rows_with_bad_indices():
+    """Tokens outside the vocabulary count as an error only inside a row's history."""
+    dev = _cuda()
+    rows, vocab = 700, 9000
+    tokens = np.random.default_rng(3).integers(0, vocab, 5000).astype(np.int32)
+    tokens[[100, 2047, 2048]] = [-1, vocab, 2 ** 31 - 1]
+    s = dict(NONE, tokens=tokens, repetition=np.full(rows, 2.0, np.float32), begin=np.full(rows, 101),
+             end=np.full(rows, 2047))
+    x = torch.randn(rows, vocab, device="cuda")
+    pulse.get_error(dev)
+    for begin, end, error in ((101, 2047, 0), (100, 200, 5), (2040, 2048, 5), (2048, 2049, 5), (2049, 5000, 0), (0, 5000, 5)):
+        s["begin"], s["end"] = np.full(rows, 0), np.full(rows, 0)
+        s["begin"][333], s["end"][333] = begin, end
+        y = plan_of(s, rows, vocab).shape(x)
+        assert pulse.get_error(dev) == error
+        want, size = ref.shape64(x[333:334].cpu().numpy(), dict(s, begin=s["begin"][333:], end=s["end"][333:]))
+        same(y[333:334], want, size, F32)
+        assert torch.equal(y[:333], x[:333]) and torch.equal(y[334:], x[334:])
+
+
+def test_many_rows_captured_in_a_graph():
+    """Without a workspace (nothing is allocated in a capture) and with one."""
+    _cuda()
+    rows, vocab = 640, 8200
+    s = settings(rows, vocab, seed=23)
+    x = torch.randn(rows, vocab, device="cuda")
+    plan = plan_of(s, rows, vocab)
+    want = plan.shape(x)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        out = torch.zeros_like(x)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                plan.shape(x, out=out)
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(out, want)
+            plan.shape(x, out=out)  # allocates the stream's workspace
+        side.synchronize()
+
+
 def test_on_another_stream():
     _cuda()
     rows, vocab = 16, 20011
