@@ -408,7 +408,7 @@ struct pulse_adam_plan {
   AdamTensorDesc* staging = nullptr;  // pinned copy that pulse_adam_plan_set_grads sends
   cudaEvent_t staged = nullptr;       // the last copy out of `staging`
   uint32_t* tile_tensor = nullptr;    // device: tensor of each tile
-  uint64_t* partials = nullptr;         // device: norm partial sums, then the ticket word
+  uint64_t* partials = nullptr;       // device: norm partial sums, then the ticket word
 };
 
 extern "C" {
@@ -1581,24 +1581,21 @@ AdamTensorDesc make_adam_desc(const pulse_adam_tensor& t, int state_bits, uint64
   return d;
 }
 
+// The plan's device tables, in one allocation: descriptors, norm scratch, tiles.
 int adam_plan_tables(pulse_adam_plan* p, const std::vector<uint32_t>& tile_tensor) {
-  const size_t desc_bytes = sizeof(AdamTensorDesc) * p->host_desc.size();
-  const size_t tile_bytes = sizeof(uint32_t) * (tile_tensor.empty() ? 1 : tile_tensor.size());
+  const size_t desc_bytes = sizeof(AdamTensorDesc) * p->host_desc.size();  // a multiple of 16
   const size_t part_bytes = sizeof(uint64_t) * (size_t(kNormMaxCtas) + 1);
-  if (cudaMalloc(&p->desc, desc_bytes) != cudaSuccess ||
-      cudaMalloc(&p->tile_tensor, tile_bytes) != cudaSuccess ||
-      cudaMalloc(&p->partials, part_bytes) != cudaSuccess ||
-      cudaMallocHost(&p->staging, desc_bytes) != cudaSuccess)
-    return PULSE_ERR_NOMEM;
-  if (cudaEventCreateWithFlags(&p->staged, cudaEventDisableTiming) != cudaSuccess ||
+  const size_t tile_bytes = sizeof(uint32_t) * tile_tensor.size();
+  char* base = nullptr;
+  if (cudaMalloc(&base, desc_bytes + part_bytes + tile_bytes) != cudaSuccess) return PULSE_ERR_NOMEM;
+  p->desc = reinterpret_cast<AdamTensorDesc*>(base);
+  p->partials = reinterpret_cast<uint64_t*>(base + desc_bytes);
+  p->tile_tensor = reinterpret_cast<uint32_t*>(base + desc_bytes + part_bytes);
+  if (cudaMemset(p->partials, 0, part_bytes) != cudaSuccess ||
       cudaMemcpy(p->desc, p->host_desc.data(), desc_bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
-      (!tile_tensor.empty() &&
-       cudaMemcpy(p->tile_tensor, tile_tensor.data(), sizeof(uint32_t) * tile_tensor.size(),
-                  cudaMemcpyHostToDevice) != cudaSuccess) ||
-      cudaMemset(p->partials, 0, part_bytes) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess)
+      (tile_bytes && cudaMemcpy(p->tile_tensor, tile_tensor.data(), tile_bytes, cudaMemcpyHostToDevice) != cudaSuccess))
     return PULSE_ERR_CUDA;
-  return PULSE_OK;
+  return cuda_status(cudaDeviceSynchronize());
 }
 
 }  // namespace
@@ -1660,9 +1657,7 @@ int pulse_adam_plan_create(const pulse_adam_tensor* tensors, int ntensors, int s
 int pulse_adam_plan_destroy(pulse_adam_plan* plan) {
   if (plan == nullptr) return PULSE_OK;
   const cudaError_t e = cudaDeviceSynchronize();
-  if (plan->desc) cudaFree(plan->desc);
-  if (plan->tile_tensor) cudaFree(plan->tile_tensor);
-  if (plan->partials) cudaFree(plan->partials);
+  if (plan->desc) cudaFree(plan->desc);  // all device tables
   if (plan->staging) cudaFreeHost(plan->staging);
   if (plan->staged) cudaEventDestroy(plan->staged);
   delete plan;
@@ -1674,6 +1669,10 @@ int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, c
   for (int i = 0; i < plan->ntensors; ++i)
     if (!grad_pointer_ok(grads[i], plan->host_desc[size_t(i)].grad_bf16 ? PULSE_BF16 : PULSE_F32))
       return PULSE_ERR_INVALID;
+  const size_t bytes = sizeof(AdamTensorDesc) * plan->host_desc.size();
+  if (plan->staged == nullptr && cudaEventCreateWithFlags(&plan->staged, cudaEventDisableTiming) != cudaSuccess)
+    return PULSE_ERR_CUDA;
+  if (plan->staging == nullptr && cudaMallocHost(&plan->staging, bytes) != cudaSuccess) return PULSE_ERR_NOMEM;
   for (int i = 0; i < plan->ntensors; ++i) {
     AdamTensorDesc& d = plan->host_desc[size_t(i)];
     d.g = grads[i];
@@ -1682,7 +1681,6 @@ int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, c
   plan->mixed = adam_mixed(plan->host_desc);
   // the copy before this one has left the pinned buffer
   if (cudaEventSynchronize(plan->staged) != cudaSuccess) return PULSE_ERR_CUDA;
-  const size_t bytes = sizeof(AdamTensorDesc) * plan->host_desc.size();
   std::memcpy(plan->staging, plan->host_desc.data(), bytes);
   if (cudaMemcpyAsync(plan->desc, plan->staging, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
     return PULSE_ERR_CUDA;
@@ -1843,25 +1841,29 @@ int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cuda
   const int sms = sm_count(device);
   logits_cut(*a, sms);
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace* ws = stream_workspace(device, stream);
-  if (ws == nullptr) return PULSE_ERR_NOMEM;
-  if (ws->counters == nullptr && stream_captured(stream)) {
-    ws = &g_capture_ws[device];
-    if (ws->counters == nullptr) ws->counters = logits_capture_counters();
-    if (ws->counters == nullptr) return PULSE_ERR_CUDA;
+  try {
+    Workspace* ws = stream_workspace(device, stream);
+    if (ws == nullptr) return PULSE_ERR_NOMEM;
+    if (ws->counters == nullptr && stream_captured(stream)) {
+      ws = &g_capture_ws[device];
+      if (ws->counters == nullptr) ws->counters = logits_capture_counters();
+      if (ws->counters == nullptr) return PULSE_ERR_CUDA;
+    }
+    const int st = workspace_reserve(*ws, 0, stream);
+    if (st != PULSE_OK) return st;
+    a->error_word = ws->counters + 2;
+    // a captured call may be replayed when the workspace has grown or is in use
+    if (!history || !logits_sorts(*a, sms) || stream_captured(stream)) return PULSE_OK;
+    LogitsWorkspace*& lw = g_logits_ws[std::make_pair(device, reinterpret_cast<uintptr_t>(stream))];
+    if (lw == nullptr) lw = new (std::nothrow) LogitsWorkspace();
+    if (lw == nullptr) return PULSE_ERR_NOMEM;
+    if (!logits_reserve(*lw, logits_sort_entries(*a), logits_sort_offs(*a), stream)) return PULSE_OK;
+    a->sorted = lw->entries;
+    a->sorted_offs = lw->offs;
+    return cuda_status(launch_logits_sort(*a, lw->entries, lw->offs, stream));
+  } catch (const std::bad_alloc&) {
+    return PULSE_ERR_NOMEM;
   }
-  const int st = workspace_reserve(*ws, 0, stream);
-  if (st != PULSE_OK) return st;
-  a->error_word = ws->counters + 2;
-  // a captured call may be replayed when the workspace has grown or is in use
-  if (!history || !logits_sorts(*a, sms) || stream_captured(stream)) return PULSE_OK;
-  LogitsWorkspace*& lw = g_logits_ws[std::make_pair(device, reinterpret_cast<uintptr_t>(stream))];
-  if (lw == nullptr) lw = new (std::nothrow) LogitsWorkspace();
-  if (lw == nullptr) return PULSE_ERR_NOMEM;
-  if (!logits_reserve(*lw, logits_sort_entries(*a), logits_sort_offs(*a), stream)) return PULSE_OK;
-  a->sorted = lw->entries;
-  a->sorted_offs = lw->offs;
-  return cuda_status(launch_logits_sort(*a, lw->entries, lw->offs, stream));
 }
 
 }  // namespace
