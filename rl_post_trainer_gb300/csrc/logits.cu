@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t lead_of(const T* p) {
   return uint32_t(0u - uint32_t(reinterpret_cast<uintptr_t>(p) / sizeof(T))) & 7u;
 }
 
-// A row's settings, read by the CTA's first warp. Ranges that do not fit their lists
+// A row's settings. Ranges that do not fit their lists
 // are empty (and recorded).
 struct RowSettings {
   const int32_t* tokens;   // the history; null where the tokens are sorted
@@ -110,44 +110,46 @@ struct RowSettings {
   float rep, inv_rep, pres, freq, inv_t;
 };
 
-// A setting a lane, so that one wait covers them all.
+// A warp for each kind of setting: what a single one would do for all holds the
+// others up at the barrier.
 __device__ __forceinline__ void read_row(const LogitsArgs& a, uint32_t row, bool history, RowSettings& r) {
-  const uint32_t lane = threadIdx.x;
-  const int64_t* p8 = nullptr;
-  const float* p4 = nullptr;
-  if (history) {
-    if (lane == 0) p8 = a.begin + row;
-    if (lane == 1) p8 = (a.split ? a.split : a.begin) + row;
-    if (lane == 2) p8 = a.end + row;
-  }
-  if (a.bias_tokens && (lane == 3 || lane == 4)) p8 = a.bias_begin + row + (lane - 3u);
-  if (lane == 5) p4 = a.repetition;
-  if (lane == 6) p4 = a.temperature;
-  if (lane == 7) p4 = a.presence;
-  if (lane == 8) p4 = a.frequency;
-  const int64_t v8 = p8 ? *p8 : 0;
-  const float v4 = p4 ? p4[row] : lane < 7 ? 1.0f : 0.0f;
-  const int64_t m = a.mask == nullptr ? -1 : a.mask_row ? int64_t(a.mask_row[row]) : int64_t(row);
-  auto i64 = [&](int k) { return __shfl_sync(0xFFFFFFFFu, v8, k); };
-  const int64_t begin = i64(0), split = i64(1), end = i64(2), bias = i64(3), bias_end = i64(4);
-  const bool h_ok = begin >= 0 && split >= begin && end >= split && end <= a.ntokens && end - begin < (1ll << 31);
-  const bool b_ok = bias >= 0 && bias_end >= bias && bias_end <= a.nbias;
-  if (lane == 0) {
-    r.tokens = a.tokens + begin;
-    r.history = h_ok ? uint32_t(end - begin) : 0u;
-    r.made = uint32_t(split - begin);
-    r.block = uint32_t(begin / kBlock);
-    r.from = uint32_t(begin % kBlock);
-    r.biased = b_ok ? uint32_t(bias_end - bias) : 0u;
-    r.bias_tokens = a.bias_tokens + bias;
-    r.bias_values = a.bias_values + bias;
+  const uint32_t lane = threadIdx.x & 31u;
+  if (threadIdx.x < 32u) {
+    const int64_t* p = lane == 0 ? a.begin : lane == 1 ? (a.split ? a.split : a.begin) : a.end;
+    const int64_t v = history && lane < 3 ? p[row] : 0;
+    const int64_t begin = __shfl_sync(0xFFFFFFFFu, v, 0), split = __shfl_sync(0xFFFFFFFFu, v, 1),
+                  end = __shfl_sync(0xFFFFFFFFu, v, 2);
+    const bool ok = begin >= 0 && split >= begin && end >= split && end <= a.ntokens && end - begin < (1ll << 31);
+    if (lane == 0) {
+      r.tokens = a.tokens + begin;
+      r.history = ok ? uint32_t(end - begin) : 0u;
+      r.made = uint32_t(split - begin);
+      r.block = uint32_t(begin / kBlock);
+      r.from = uint32_t(begin % kBlock);
+      if (!ok) record_error(a.error_word, kErrIndex);
+    }
+  } else if (threadIdx.x < 64u) {
+    const int64_t v = a.bias_tokens && lane < 2 ? a.bias_begin[row + lane] : 0;
+    const int64_t begin = __shfl_sync(0xFFFFFFFFu, v, 0), end = __shfl_sync(0xFFFFFFFFu, v, 1);
+    const bool ok = begin >= 0 && end >= begin && end <= a.nbias;
+    if (lane == 0) {
+      r.biased = ok ? uint32_t(end - begin) : 0u;
+      r.bias_tokens = a.bias_tokens + begin;
+      r.bias_values = a.bias_values + begin;
+      if (!ok) record_error(a.error_word, kErrIndex);
+    }
+  } else if (threadIdx.x < 96u) {
+    const float* p = lane == 0 ? a.repetition : lane == 1 ? a.temperature : lane == 2 ? a.presence : a.frequency;
+    const float v = lane < 4 && p ? p[row] : lane < 2 ? 1.0f : 0.0f;
+    if (lane == 0) r.rep = v, r.inv_rep = __frcp_rn(v);
+    if (lane == 1) r.inv_t = v > 0.0f ? __frcp_rn(v) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
+    if (lane == 2) r.pres = v;
+    if (lane == 3) r.freq = v;
+  } else if (threadIdx.x == 96u) {
+    const int64_t m = a.mask == nullptr ? -1 : a.mask_row ? int64_t(a.mask_row[row]) : int64_t(row);
     r.mask = m >= 0 && m < a.mask_rows ? a.mask + uint64_t(m) * a.mask_stride : nullptr;
-    if (!h_ok || !b_ok || (a.mask && m >= a.mask_rows)) record_error(a.error_word, kErrIndex);
+    if (a.mask && m >= a.mask_rows) record_error(a.error_word, kErrIndex);
   }
-  if (lane == 5) r.rep = v4, r.inv_rep = __frcp_rn(v4);
-  if (lane == 6) r.inv_t = v4 > 0.0f ? __frcp_rn(v4) : 1.0f;  // not above 0, greedy decoding: the row stays as it is
-  if (lane == 7) r.pres = v4;
-  if (lane == 8) r.freq = v4;
 }
 
 // This CTA's part of a row: tokens [first, stop), groups from `base` on, up to 7
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
   if (s.row >= a.rows) return;
   Groups<TIn> g;
   g.load(s, src);
-  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
+  read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
   __syncthreads();
   const uint32_t* mask = row.mask;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   if (s.row >= a.rows) return;
   Groups<TIn> g;
   g.load(s, src);
-  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
+  read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(cons
   if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
   Groups<TOut> g;
   g.load(s, src);
-  if (threadIdx.x < 32u) read_row(a, s.row, history, row);
+  read_row(a, s.row, history, row);
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
   __syncthreads();
   const uint32_t* mask = row.mask;
