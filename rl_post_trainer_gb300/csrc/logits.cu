@@ -15,19 +15,13 @@
 namespace pulse {
 namespace {
 
-#ifndef PULSE_LOGITS_GROUPS
-#define PULSE_LOGITS_GROUPS 4
-#endif
-#ifndef PULSE_LOGITS_THREADS
-#define PULSE_LOGITS_THREADS 256
-#endif
-constexpr int kThreads = PULSE_LOGITS_THREADS;
+constexpr int kThreads = 256;
 // CTAs per SM: as many as the registers of a slice's groups leave without spilling.
 template <typename TSrc>
 constexpr int kMinCtas = sizeof(TSrc) == 4 ? 4 : 5;
 // Groups of 8 elements a thread holds: its whole part of a slice, asked for
 // before the history is read.
-constexpr int kGroups = PULSE_LOGITS_GROUPS;
+constexpr int kGroups = 4;
 constexpr uint32_t kSliceMin = 2048;
 constexpr uint32_t kRound = 8u * kThreads;  // tokens of a group a thread
 constexpr uint32_t kSliceMax = kRound * kGroups;
@@ -496,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   // generated; where its bit in `final` is set, the logit with penalties and bias
   __shared__ __align__(16) uint32_t word[kPlaces];
   __shared__ uint32_t final[kWords], open[kWords];
+  __shared__ uint32_t twice;  // a token of the bias list is listed twice
   __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
   TOut* dst = static_cast<TOut*>(a.dst);
@@ -505,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   Groups<TIn> g;
   g.load(s, src);
   read_row(a, s.row, history, row);
+  if (threadIdx.x == 0) twice = 0u;
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -512,16 +508,27 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  // Every warp reads the bias list backwards, 32 entries at a time, and serves the
-  // places that are its own: the last entry of a token comes first, and its bit in
-  // `final` turns the others away. The latest entries are asked for before the
-  // history is read.
-  constexpr int kAhead = 4;
-  const uint32_t biased = row.biased;
-  uint32_t ahead[kAhead];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    ahead[k] = lane + 32u * k < biased ? uint32_t(row.bias_tokens[biased - 1u - lane - 32u * k]) : 0xFFFFFFFFu;
+  // A bias list of at most an entry a thread is read here, with the logit and the
+  // value that an entry in the slice needs; bits in `final` claim its tokens. A token
+  // listed twice is met there and sends the whole list the slow way, which longer
+  // lists go anyhow. (256 rows of 151,936 with up to 256 biases each: 59 us when every
+  // list went the slow way, 54 us so, 56 us with two entries a thread.)
+  const uint32_t biased = row.biased, len = s.stop - s.first, off = s.first - s.base + 8u;
+  const bool quick = biased <= uint32_t(kThreads);
+  uint32_t mine = 0u;  // place of this thread's entry, 0: none
+  float logit, value;
+  if (quick && threadIdx.x < biased) {
+    const uint32_t t = uint32_t(row.bias_tokens[threadIdx.x]);
+    if (t - s.first < len) {
+      mine = t - s.first + off;
+      logit = load_elem(src + t);
+      value = row.bias_values[threadIdx.x];
+      const uint32_t bit = 1u << (mine & 31u);
+      if (atomicOr(final + (mine >> 5), bit) & bit) twice = 1u;
+    } else if (t >= a.vocab) {
+      record_error(a.error_word, kErrIndex);
+    }
+  }
   const float rep = row.rep, inv_rep = row.inv_rep, freq = row.freq, pres = row.pres, inv_t = row.inv_t;
   auto penalized = [&](float x, uint32_t st) {
     const uint32_t made = st & 0x7FFFFFFFu;
@@ -538,30 +545,35 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
         or_if(x.in[k] && !x.made[k], word + x.u[k], 0x80000000u);
       }
     });
-    if (biased) __syncthreads();
   }
   if (biased) {
-    const uint32_t len = s.stop - s.first, off = s.first - s.base + 8u;
-    uint32_t bad = 0u;
-    // a warp's lanes together, the entry `back` from the end; the lowest lane has the latest
-    auto serve = [&](uint32_t t, uint32_t back) {
-      bad |= back < biased && t >= a.vocab;
-      const uint32_t u = t - s.first + off;
-      const bool own = t - s.first < len && u * (kThreads / 32u) / kPlaces == warp;
-      const uint32_t owners = __ballot_sync(0xFFFFFFFFu, own);
-      if (!own) return;
-      const uint32_t same = __match_any_sync(owners, u), bit = 1u << (u & 31u);
-      if (lane != uint32_t(__ffs(same) - 1)) return;
-      if (atomicOr(final + (u >> 5), bit) & bit) return;
-      const float x = load_elem(src + (s.base + u - 8u));
-      word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, row.bias_values[biased - 1u - back]));
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (biased > 32u * k) serve(ahead[k], lane + 32u * k);
-    for (uint32_t back = 32u * kAhead; back < biased; back += 32u)
-      serve(back + lane < biased ? uint32_t(row.bias_tokens[biased - 1u - back - lane]) : 0xFFFFFFFFu, back + lane);
-    if (bad) record_error(a.error_word, kErrIndex);
+    __syncthreads();
+    if (quick && !twice) {
+      if (mine) {
+        const uint32_t st = word[mine];
+        word[mine] = __float_as_uint(__fadd_rn(st ? penalized(logit, st) : logit, value));
+      }
+    } else {
+      // Every warp reads the list backwards, 32 entries at a time, and serves the
+      // places that are its own: the last entry of a token comes first, and its bit
+      // turns the others away.
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
+      __syncthreads();
+      for (uint32_t back = lane; back - lane < biased; back += 32u) {
+        const uint32_t i = biased - 1u - back;
+        const uint32_t t = back < biased ? uint32_t(row.bias_tokens[i]) : 0xFFFFFFFFu, u = t - s.first + off;
+        if (back < biased && t >= a.vocab) record_error(a.error_word, kErrIndex);
+        const bool own = t - s.first < len && u * (kThreads / 32u) / kPlaces == warp;
+        const uint32_t owners = __ballot_sync(0xFFFFFFFFu, own);
+        if (!own) continue;
+        const uint32_t same = __match_any_sync(owners, u), bit = 1u << (u & 31u);
+        if (lane != uint32_t(__ffs(same) - 1)) continue;  // a lane with a later entry
+        if (atomicOr(final + (u >> 5), bit) & bit) continue;
+        const float x = load_elem(src + (s.base + u - 8u));
+        word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, row.bias_values[i]));
+      }
+    }
   }
   mask_ready();
   __syncthreads();

@@ -1227,7 +1227,7 @@ class _on_device:
         self.index, self.back = dev.index, None
 
     def __enter__(self):
-        now = torch.cuda.current_device()
+        now = torch._C._cuda_getDevice()
         if now != self.index:
             self.back = now
             torch.cuda.set_device(self.index)
@@ -1469,21 +1469,23 @@ class LogitsPlan:
         self._ref = ctypes.byref(self._c)
 
     def _rows_of(self, t: torch.Tensor, name: str, dtypes, like: Optional[torch.Tensor] = None):
+        """(pointer, pitch in elements) of rows of logits or their gradient."""
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name}: expected a CUDA tensor")
         if t.dtype not in dtypes:
             raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-        if t.dim() != 2 or t.shape[1] != self.vocab or t.shape[0] > self.rows:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [<= {self.rows}, {self.vocab}]")
-        if t.stride(1) != 1 and self.vocab > 1:
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 2 or shape[1] != self.vocab or shape[0] > self.rows:
+            raise ValueError(f"{name}: shape {tuple(shape)}, expected [<= {self.rows}, {self.vocab}]")
+        if stride[1] != 1 and self.vocab > 1:
             raise ValueError(f"{name}: rows must be contiguous")
-        if like is not None and t.shape[0] != like.shape[0]:
-            raise ValueError(f"{name}: {t.shape[0]} rows, expected {like.shape[0]}")
+        if like is not None and shape[0] != like.shape[0]:
+            raise ValueError(f"{name}: {shape[0]} rows, expected {like.shape[0]}")
         if self.device is None:
             self.device = t.device
-        if t.device != self.device:
+        elif t.device != self.device:
             raise ValueError(f"{name}: on {t.device}, expected {self.device}")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), self.vocab)
+        return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], self.vocab)
 
     def shape(self, logits: torch.Tensor, out: Optional[torch.Tensor] = None,
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:

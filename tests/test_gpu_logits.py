@@ -199,6 +199,22 @@ def test_token_biased_twice_takes_the_last_entry():
         check(s, 2, 10, F32, F32)
 
 
+@pytest.mark.parametrize("rows", [2, 310])
+@pytest.mark.parametrize("per_row", [255, 256, 257, 1000, 9001])
+def test_long_bias_lists(rows, per_row):
+    """Distinct tokens; in the last row one of them a second time, its first entry to be ignored."""
+    _cuda()
+    vocab = 9001
+    s = settings(rows, vocab, seed=24, bias=0)
+    g = np.random.default_rng(per_row)
+    each = [g.permutation(vocab)[:per_row] for _ in range(rows)]
+    each[-1] = np.append(each[-1], each[-1][per_row // 2])
+    s["bias_tokens"] = np.concatenate(each).astype(np.int32)
+    s["bias_values"] = g.normal(0, 5, s["bias_tokens"].size).astype(np.float32)
+    s["bias_begin"] = np.cumsum([0] + [len(e) for e in each])
+    check(s, rows, vocab, BF16, F32)
+
+
 @pytest.mark.parametrize("tin,tout", PAIRS)
 def test_special_values(tin, tout):
     """Infinities and NaN, in masked places and open ones; the type's lowest value; zeros of both signs."""
