@@ -464,9 +464,8 @@ __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptr
   }
 }
 
-// A tile is 8,192 elements, four blocks a warp (1.54 billion parameters with BF16
-// gradients: 3.41 ms, 6.3 TB/s; one block a warp 3.60 ms), or 2,048 in plans too
-// small to fill the SMs with the larger.
+// A tile is one, two or four blocks a warp, by the size of the plan. 1.54 billion
+// parameters with BF16 gradients: 3.41 ms, 6.3 TB/s.
 // MIXED: some tensor of the plan is not aligned for groups throughout. The kernel
 // for aligned plans keeps its registers without the code for the others (3.41 ms
 // against 3.48 with both in one). The other way of the general one serves whole

@@ -1551,13 +1551,16 @@ bool adam_mixed(const std::vector<AdamTensorDesc>& desc) {
   return false;
 }
 
-// 8-bit moments: a warp takes tile / 2048 blocks one after the other. Four of
-// them hide the table lookups (the 1.5B-parameter step 3.38 ms against 3.85 with
-// one), as long as every SM still has two CTAs; below that one block a warp is
-// faster (200,000 parameters: 7.9 against 10.3 us, 1,000,000: 8.7 against 8.8).
+// 8-bit moments: a warp takes tile / 2048 blocks one after the other, which hides
+// the waits of one behind another's, as long as the SMs are full: the step of 1.54
+// billion parameters takes 3.41 ms with four blocks and 3.60 with one. A plan that
+// leaves an SM fewer than its four CTAs takes one block (1 million parameters with
+// the export: 14.4 us, 16.4 with two), one that gives it few rounds of them takes two
+// (3 million: 25.7 us, 26.9 with four, 27.2 with one; 25 million: 115.5, 112.2, 130.8).
 uint32_t adam_tile(uint64_t total, int state_bits, int sms) {
   if (state_bits == 32) return kAdam32Tile;
-  return total < uint64_t(kAdam8Tile) * 2 * uint64_t(sms) ? kAdam8TileSmall : kAdam8Tile;
+  if (total < uint64_t(kAdam8TileMin) * 4 * uint64_t(sms)) return kAdam8TileMin;
+  return total < uint64_t(kAdam8TileMax) * 8 * uint64_t(sms) ? 2 * kAdam8TileMin : kAdam8TileMax;
 }
 
 AdamTensorDesc make_adam_desc(const pulse_adam_tensor& t, int state_bits, uint64_t tile_begin,

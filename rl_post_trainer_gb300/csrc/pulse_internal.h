@@ -349,8 +349,8 @@ cudaError_t launch_xor_apply(const TensorDesc& one, const TensorDesc* tensors,
 constexpr int kAdamBlock = 256;      // elements sharing an exponent byte (8-bit moments)
 constexpr int kAdamThreads = 256;
 constexpr uint32_t kAdam32Tile = 2048;  // elements per CTA, FP32 moments
-constexpr uint32_t kAdam8Tile = 8192;       // 8-bit moments
-constexpr uint32_t kAdam8TileSmall = 2048;  // 8-bit moments, small plans
+constexpr uint32_t kAdam8TileMin = 2048;  // 8-bit moments, a block a warp
+constexpr uint32_t kAdam8TileMax = 8192;
 
 struct alignas(16) AdamTensorDesc {  // read in 16-byte pieces
   float* w;

@@ -39,7 +39,8 @@ class Shifted:
 class Model:
     """Tensors of a plan and their numpy state."""
 
-    def __init__(self, sizes, bits, grad=torch.float32, shift=0, seed=0, missing=(), scale=1e-3):
+    def __init__(self, sizes, bits, grad=torch.float32, shift=0, seed=0, missing=(), scale=1e-3, codes=None):
+        """codes: where the 8-bit codes start, if not where the others do."""
         g = torch.Generator().manual_seed(seed)
         self.bits, self.sizes, self.parts = bits, sizes, []
         self.wd = [0.01 if i % 2 else 0.0 for i in range(len(sizes))]
@@ -65,7 +66,7 @@ class Model:
                 for k, x, signed in (("m", m, True), ("v", v, False)):
                     c, e = ref.encode8(x.numpy(), np.full(n, 32768), signed)
                     p[k], p[k + "_exp"] = c, e
-                    p["buf"][k] = Shifted(torch.from_numpy(c), torch.uint8, shift)
+                    p["buf"][k] = Shifted(torch.from_numpy(c), torch.uint8, shift if codes is None else codes)
                     p["buf"][k + "_exp"] = Shifted(torch.from_numpy(e), torch.uint8, shift % 3)
                     p["buf"][k + "_out"] = Shifted(torch.zeros(n), torch.float32, shift)
                 kw = {k: p["buf"][k].t for k in ("m_exp", "v_exp", "m_out", "v_out")}
@@ -130,6 +131,23 @@ def test_single_tensor(bits, n):
     model = Model([n], bits, torch.bfloat16, seed=n)
     model.step(5, 0.5, seed=n)
     model.check()
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("total", [1200000, 1300021, 10000000, 10700009])
+def test_eight_bit_plans_of_each_tile(total, shift, grad):
+    """One, two and four blocks a warp on a GPU of 152 SMs, with the last tiles of the tensors cut anywhere."""
+    _cuda()
+    model = Model([total // 3 + 1, 777, total // 2, 256, total - total // 3 - total // 2], 8, grad, shift, seed=total,
+                  codes=0)
+    model.step(9, 0.5, seed=total << 3)
+    model.plan.export_states()
+    model.check()
+    for p in model.parts:
+        for k, signed in (("m", True), ("v", False)):
+            out = p["buf"][k + "_out"].t.cpu().numpy()
+            np.testing.assert_array_equal(out, ref.decode8(p[k], p[k + "_exp"], signed).astype(np.float32))
 
 
 @pytest.mark.parametrize("bits", [32, 8])
