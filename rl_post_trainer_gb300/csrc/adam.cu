@@ -567,11 +567,12 @@ __device__ __forceinline__ Sum2 block_sum(Sum2 x, Sum2* smem) {
 
 // Sum of the squares of elements [lo, hi) of one tensor, this thread's share.
 // Plain FP32 over the 8 * kNormUnroll elements that one turn loads.
-constexpr int kNormUnroll = 2;
-// CTAs per SM, all resident at once: the ranges are equal, so a second wave
-// would leave SMs idle. Of 4 x 4 loads, 6 x 4, 8 x 2 and 6 x 2 the last was the
-// fastest on the 1.5B-parameter set in BF16 (501, 500, 486 and 477 us).
-constexpr int kNormCtas = 6;
+constexpr int kNormUnroll = 4;
+// CTAs per SM, all resident at once. With 4 loads a turn 4, 5 and 6 take 449, 434
+// and 437 us for 1.54 billion BF16 gradients; 6 with 2 loads take 465.
+constexpr int kNormCtas = 5;
+// Elements that a CTA takes at a time.
+constexpr uint32_t kNormPiece = 65536;
 
 template <bool BF16>
 __device__ __forceinline__ Sum2 sum_squares(const void* g, uint64_t lo, uint64_t hi) {
@@ -635,26 +636,30 @@ __device__ __forceinline__ Sum2 sum_squares(const void* g, uint64_t lo, uint64_t
   return sum;
 }
 
-// Each CTA sums a fixed range of tiles, tensor by tensor; the CTA that finishes
+// The tiles are cut into equal pieces, as many for one CTA as for another, and the
+// CTAs go through the gradients side by side, piece by piece. The CTA that finishes
 // last adds the partial sums in CTA order, so the result does not depend on the
 // schedule. Each gradient is read once and nothing else: bound by memory. 1.54
-// billion BF16 gradients: 477 us, 6.5 TB/s; the smallest call is a launch and two
-// trips to memory, 6.2 us.
+// billion BF16 gradients: 434 us, 7.1 TB/s (477 us with one long piece a CTA, whose
+// distant streams the memory serves less well, 458 us with pieces of 131,072); the
+// smallest call is a launch and four trips to memory one after the other, 6 us.
 __global__ void __launch_bounds__(kAdamThreads, kNormCtas)
     grad_norm_kernel(const AdamTensorDesc* tensors, const uint32_t* tile_tensor, uint32_t tile,
-                     uint64_t total_tiles, Sum2* partials, uint32_t* ticket, float max_norm,
+                     uint64_t total_tiles, uint64_t pieces, Sum2* partials, uint32_t* ticket, float max_norm,
                      float* norm_out, float* clip_out) {
   __shared__ Sum2 smem[kAdamThreads / 32];
   __shared__ bool last;
-  const uint64_t hi = total_tiles * (blockIdx.x + 1) / gridDim.x;
   Sum2 sum{0.0f, 0.0f};
-  for (uint64_t t = total_tiles * blockIdx.x / gridDim.x; t < hi;) {
-    const AdamTensorDesc& d = tensors[tile_tensor[t]];
-    const uint64_t begin = d.tile_begin, n = d.n;
-    const uint64_t e0 = (t - begin) * tile, e1 = min((hi - begin) * tile, n);
-    if (d.g != nullptr)
-      sum = add_sum(sum, d.grad_bf16 ? sum_squares<true>(d.g, e0, e1) : sum_squares<false>(d.g, e0, e1));
-    t = begin + (n + tile - 1) / tile;
+  for (uint64_t piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+    const uint64_t hi = total_tiles * (piece + 1) / pieces;
+    for (uint64_t t = total_tiles * piece / pieces; t < hi;) {
+      const AdamTensorDesc& d = tensors[tile_tensor[t]];
+      const uint64_t begin = d.tile_begin, n = d.n;
+      const uint64_t e0 = (t - begin) * tile, e1 = min((hi - begin) * tile, n);
+      if (d.g != nullptr)
+        sum = add_sum(sum, d.grad_bf16 ? sum_squares<true>(d.g, e0, e1) : sum_squares<false>(d.g, e0, e1));
+      t = begin + (n + tile - 1) / tile;
+    }
   }
   sum = block_sum(sum, smem);
   if (threadIdx.x == 0) {
@@ -716,8 +721,10 @@ cudaError_t launch_grad_norm(const AdamTensorDesc* tensors, const uint32_t* tile
   uint64_t grid = uint64_t(sms) * kNormCtas;
   if (grid > uint64_t(kNormMaxCtas)) grid = kNormMaxCtas;
   if (grid > total_tiles) grid = total_tiles ? total_tiles : 1;
+  const uint64_t turn = grid * (kNormPiece / tile);
+  const uint64_t pieces = grid * ((total_tiles + turn - 1) / turn);
   grad_norm_kernel<<<unsigned(grid), kAdamThreads, 0, stream>>>(
-      tensors, tile_tensor, tile, total_tiles, reinterpret_cast<Sum2*>(partials), ticket, max_norm, norm_out, clip_out);
+      tensors, tile_tensor, tile, total_tiles, pieces, reinterpret_cast<Sum2*>(partials), ticket, max_norm, norm_out, clip_out);
   return cudaGetLastError();
 }
 

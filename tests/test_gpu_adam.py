@@ -328,7 +328,8 @@ NORM_TOL = 2.0 ** -19 + 2.0 ** -24
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("sizes", [[1], [7], [255, 1, 0, 4096], [4097, 100003, 5], [1 << 20], [3333333, 17, 262144]])
+@pytest.mark.parametrize("sizes", [[1], [7], [255, 1, 0, 4096], [4097, 100003, 5], [1 << 20], [3333333, 17, 262144],
+                                   [40000003, 1 << 20, 77, 60000001]])
 def test_norm_and_clip(dtype, sizes):
     _cuda()
     gen = torch.Generator(device="cuda").manual_seed(len(sizes) + sizes[0])
