@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   __syncthreads();
   if (threadIdx.x < 32) {
     uint32_t sum = 0u;
-    for (uint32_t w = 0; w < 256; w += 32) {
+    for (uint32_t w = 0; w < slices + 2u; w += 32) {
       const uint32_t own = count[w + threadIdx.x];
       uint32_t x = own;
 #pragma unroll
@@ -345,13 +345,22 @@ __device__ __forceinline__ void or_if(bool p, uint32_t* at, uint32_t x) {
                : "memory");
 }
 
-// Sets the bits of the history.
+__device__ __forceinline__ void prefetch_if(bool p, const void* at) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p prefetch.global.L2 [%1];\n\t}" ::"r"(uint32_t(p)),
+               "l"(at));
+}
+
+// Sets the bits of the history. Where the tokens' elements of a second row are needed
+// next, `near` is that row at place 0, and they are asked for here.
+template <typename T = void>
 __device__ __forceinline__ void mark_history(const LogitsArgs& a, const Slice& s, const RowSettings& row,
-                                             uint32_t* bits) {
+                                             uint32_t* bits, const T* near = nullptr) {
   scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (!std::is_void_v<T>) prefetch_if(x.in[k], near + x.u[k]);
       or_if(x.in[k], bits + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
+    }
   });
 }
 
@@ -639,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(cons
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
   sorted_ready();
-  if (row.history) mark_history(a, s, row, bits);
+  if (row.history) mark_history(a, s, row, bits, raw + int64_t(s.base) - 8);
   mask_ready();
   __syncthreads();
   const float inv_t = row.inv_t, rep = row.rep, inv_rep = row.inv_rep;
