@@ -867,8 +867,8 @@ int pulse_adam_export_multi(pulse_adam_plan *plan, cudaStream_t stream);
  * on (split NULL: all of it generated). Rows may share or overlap ranges, as the
  * positions of one training sequence do.
  *
- * With many rows a call first sorts the tokens by where in the vocabulary they
- * fall, into a library workspace per (device, stream) of about 4 bytes a token,
+ * With many rows and tokens a call first sorts the tokens by where in the
+ * vocabulary they fall, into a library workspace per (device, stream) of about 4 bytes a token,
  * allocated on first use and grown on demand (growth synchronises `stream`).
  * Nothing of it is kept for the next call. A call that is being captured into a
  * graph, and one without room, works on the tokens as they are. Errors of a stream

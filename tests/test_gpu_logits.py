@@ -336,8 +336,7 @@ def test_bad_indices_are_left_out_and_recorded():
     assert torch.equal(y[:2], x[:2]) and (y[2] == -float("inf")).all()
 
 
-# With many CTAs' worth of rows the tokens are sorted by vocabulary slice first, in blocks of 2048
-# positions; the vocabularies here give two slices and more.
+# Many CTAs' worth of rows, with two slices a row and more
 @pytest.mark.parametrize("tin,tout", PAIRS)
 @pytest.mark.parametrize("vocab", [16384, 20011, 24600])
 def test_many_rows(tin, tout, vocab):
@@ -347,7 +346,7 @@ def test_many_rows(tin, tout, vocab):
 
 
 @pytest.mark.parametrize("history", [1, 2047, 2048, 2049, 9000])
-def test_many_rows_at_the_edges_of_sorted_blocks(history):
+def test_many_rows_at_the_edges_of_blocks(history):
     """Histories that begin, split and end around block boundaries, and rows that share them."""
     _cuda()
     rows, vocab = 610, 8500
@@ -418,6 +417,89 @@ def test_many_rows_captured_in_a_graph():
             assert torch.equal(out, want)
             plan.shape(x, out=out)  # allocates the stream's workspace
         side.synchronize()
+
+
+# Long token lists are sorted by vocabulary slice first, in blocks of 2048 positions. The vocabulary
+# here has 135 slices, so that some 130,000 tokens and 12 rows are enough.
+WIDE = 1100000
+
+
+@pytest.mark.parametrize("tin,tout", PAIRS)
+@pytest.mark.parametrize("vocab", [WIDE, WIDE + 3])
+@pytest.mark.parametrize("keys", [(), ("frequency", "presence", "bias_tokens", "bias_values", "bias_begin")])
+def test_sorted_histories(tin, tout, vocab, keys):
+    _cuda()
+    s = settings(12, vocab, history=60000, seed=31, bias=40, **{k: None for k in keys})
+    assert s["tokens"].size > 130000
+    check(s, 12, vocab, tin, tout)
+
+
+@pytest.mark.parametrize("history", [1, 2047, 2048, 2049, 9000, 100000])
+def test_sorted_histories_at_the_edges_of_blocks(history):
+    _cuda()
+    rows = 12
+    g = np.random.default_rng(history)
+    total = 131072 + 4200
+    s = settings(rows, WIDE, seed=32, bias=3)
+    s["tokens"] = np.minimum(np.exp(g.random(total) * np.log(WIDE)).astype(np.int64) - 1, WIDE - 1).clip(0).astype(np.int32)
+    s["begin"] = g.integers(0, 4200, rows)
+    s["begin"][:8] = [0, 2047, 2048, 2049, 4095, 4096, total - history, total]
+    s["end"] = s["begin"] + history
+    s["end"][7] = s["begin"][7]
+    s["split"] = s["begin"] + (np.arange(rows) * 37) % (history + 1)
+    s["split"][7] = s["begin"][7]
+    check(s, rows, WIDE, F32, F32)
+
+
+def test_sorted_history_of_one_sequence():
+    _cuda()
+    rows, total = 12, 140000
+    s = settings(rows, WIDE, seed=33)
+    s["tokens"] = np.random.default_rng(1).integers(0, 5000, total).astype(np.int32)
+    s["begin"] = np.zeros(rows, np.int64)
+    s["end"] = np.arange(1, rows + 1) * (total // rows)
+    s["split"] = np.minimum(s["end"], 20000)
+    check(s, rows, WIDE, BF16, BF16)
+
+
+def test_sorted_histories_with_bad_indices():
+    dev = _cuda()
+    rows = 12
+    tokens = np.random.default_rng(3).integers(0, WIDE, 140000).astype(np.int32)
+    tokens[[100, 2047, 2048]] = [-1, WIDE, 2 ** 31 - 1]
+    s = dict(NONE, tokens=tokens, repetition=np.full(rows, 2.0, np.float32))
+    x = torch.randn(rows, WIDE, device="cuda")
+    pulse.get_error(dev)
+    for begin, end, error in ((101, 2047, 0), (100, 200, 5), (2040, 2048, 5), (2048, 2049, 5), (2049, 140000, 0), (0, 5000, 5)):
+        s["begin"], s["end"] = np.full(rows, 0), np.full(rows, 0)
+        s["begin"][3], s["end"][3] = begin, end
+        y = plan_of(s, rows, WIDE).shape(x)
+        assert pulse.get_error(dev) == error
+        want, size = ref.shape64(x[3:4].cpu().numpy(), dict(s, begin=s["begin"][3:], end=s["end"][3:]))
+        same(y[3:4], want, size, F32)
+        assert torch.equal(y[:3], x[:3]) and torch.equal(y[4:], x[4:])
+
+
+def test_sorted_and_captured_calls_agree():
+    """Nothing is sorted in a capture; the results have the same bits."""
+    _cuda()
+    rows = 12
+    s = settings(rows, WIDE, history=60000, seed=34)
+    x = torch.randn(rows, WIDE, device="cuda")
+    d = torch.randn(rows, WIDE, device="cuda")
+    plan = plan_of(s, rows, WIDE)
+    want, back = plan.shape(x), plan.backward(d, logits=x)
+    out, dx = torch.zeros_like(x), torch.zeros_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            plan.shape(x, out=out)
+            plan.backward(d, logits=x, out=dx)
+        graph.replay()
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(dx, back)
 
 
 def test_on_another_stream():
