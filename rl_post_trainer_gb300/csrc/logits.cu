@@ -504,18 +504,19 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
 // Everything: tokens are counted and biased.
 //   y = (p(x) - f * n - (n > 0 ? presence : 0) + b) * (1/T), p(x) as above, n the times
 //   that the token was generated, -inf where the mask is closed
-// A word a place is zeroed and read for every logit, whether or not a list names it:
-// keeping only the named ones' words took a second pass over the history and a third
-// barrier, 66 us for the case below. Instructions and the waits between the barriers
-// bound it (issue slots 47 %, DRAM 21 %): 256 BF16 rows of 128,256 with histories up to
-// 8,192, 100 biases and half of the rows masked take 54 us, 33 us without lists and
-// masks, where the logits alone would move in 20.
+// A word a place is zeroed for all logits and read for groups of 8 with a token that a
+// list names (1,024 rows with up to 64 tokens each: 95 us, 103 when all were read).
+// Zeroing the named ones alone took a second pass over the history and a third barrier,
+// and was slower everywhere. Instructions and the waits between the barriers bound this
+// kernel (issue slots 47 %, DRAM 21 %): 256 BF16 rows of 128,256 with histories up to
+// 8,192, 100 biases and half of the rows masked take 53 us, 29 us with up to 64 tokens
+// and neither biases nor masks, where the logits alone would move in 20.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __grid_constant__ LogitsArgs a) {
-  // a word a place: bit 31 for a token of the prompt, below it the times it was
-  // generated; where its bit in `final` is set, the logit with penalties and bias
+  // a word a place: the times that the token was generated; where its bit in `final`
+  // is set, the logit with penalties and bias. `used`: the tokens of the history
   __shared__ __align__(16) uint32_t word[kPlaces];
-  __shared__ uint32_t final[kWords], open[kWords];
+  __shared__ uint32_t used[kWords], final[kWords], open[kWords];
   __shared__ uint32_t twice;  // a token of the bias list is listed twice
   __shared__ RowSettings row;
   const TIn* src = static_cast<const TIn*>(a.src);
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   g.load(s, src);
   read_row(a, s.row, history, row);
   if (threadIdx.x == 0) twice = 0u;
-  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = 0u;
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = used[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
@@ -556,28 +557,25 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
     }
   }
   const float rep = row.rep, inv_rep = row.inv_rep, freq = row.freq, pres = row.pres, inv_t = row.inv_t;
-  auto penalized = [&](float x, uint32_t st) {
-    const uint32_t made = st & 0x7FFFFFFFu;
+  auto penalized = [&](float x, uint32_t made) {
     x = __fmul_rn(x, x > 0.0f ? inv_rep : rep);
     return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(made))), pres);
   };
+  auto seen = [&](uint32_t u) { return (used[u >> 5] >> (u & 31u)) & 1u; };
   sorted_ready();
   if (row.history) {
     scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         add_if(x.in[k] && x.made[k], word + x.u[k], 1u);
-        or_if(x.in[k] && !x.made[k], word + x.u[k], 0x80000000u);
+        or_if(x.in[k], used + (x.u[k] >> 5), 1u << (x.u[k] & 31u));
       }
     });
   }
   if (biased) {
     __syncthreads();
     if (quick && !twice) {
-      if (mine) {
-        const uint32_t st = word[mine];
-        word[mine] = __float_as_uint(__fadd_rn(st ? penalized(logit, st) : logit, value));
-      }
+      if (mine) word[mine] = __float_as_uint(__fadd_rn(seen(mine) ? penalized(logit, word[mine]) : logit, value));
     } else {
       // Every warp reads the list backwards, 32 entries at a time, and serves the
       // places that are its own: the last entry of a token comes first, and its bit
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
         if (lane != uint32_t(__ffs(same) - 1)) continue;  // a lane with a later entry
         if (atomicOr(final + (u >> 5), bit) & bit) continue;
         const float x = load_elem(src + (s.base + u - 8u));
-        word[u] = __float_as_uint(__fadd_rn(word[u] ? penalized(x, word[u]) : x, row.bias_values[i]));
+        word[u] = __float_as_uint(__fadd_rn(seen(u) ? penalized(x, word[u]) : x, row.bias_values[i]));
       }
     }
   }
@@ -612,13 +610,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
       float x[8];
       values(g.x[r], x);
       const uint32_t fin = reinterpret_cast<const uint8_t*>(final)[q + 1u];
-      const uint4 lo = reinterpret_cast<const uint4*>(word)[2u * q + 2u];
-      const uint4 hi = reinterpret_cast<const uint4*>(word)[2u * q + 3u];
-      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      if ((w[0] | w[1] | w[2]) | (w[3] | w[4] | w[5]) | (w[6] | w[7] | fin)) {
+      const uint32_t hit = reinterpret_cast<const uint8_t*>(used)[q + 1u];
+      if (fin | hit) {
+        const uint4 lo = reinterpret_cast<const uint4*>(word)[2u * q + 2u];
+        const uint4 hi = reinterpret_cast<const uint4*>(word)[2u * q + 3u];
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if (w[k]) x[k] = penalized(x[k], w[k]);
+          if ((hit >> k) & 1u) x[k] = penalized(x[k], w[k]);
         }
         if (fin) {
 #pragma unroll
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
       float x = load_elem(src + t);
       if ((final[u >> 5] >> (u & 31u)) & 1u)
         x = __uint_as_float(word[u]);
-      else if (word[u])
+      else if (seen(u))
         x = penalized(x, word[u]);
       y = __fmul_rn(x, inv_t);
     }
