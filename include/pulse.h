@@ -821,9 +821,9 @@ int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
  * pulse_grad_norm_multi -- norm_out[0] = sqrt(sum of the squares of every
  * gradient of the plan); clip_out[0] = min(1, max_norm / (norm + 1e-6)), or NaN
  * where the norm is not finite, so that a step given clip_out as grad_scale is
- * skipped. Squares are summed in FP32 over 16 elements and in pairs of FP32
- * numbers (about 48 bits) from there on, in an order that depends on the sizes
- * and the device alone: the same gradients give the same bits. A sum of squares
+ * skipped. Squares are summed in FP32 over 32 elements and in pairs of FP32
+ * numbers (about 48 bits) from there on, in an order that depends on the sizes,
+ * alignments and the device alone: the same gradients give the same bits. A sum of squares
  * past FP32's range (gradients above about 1e18) gives a norm that is not finite.
  *   norm_out, clip_out  device, one float each; clip_out may be NULL
  *   max_norm            >= 0 (infinity: never clips)
