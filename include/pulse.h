@@ -744,8 +744,9 @@ int pulse_encode_noalloc(const float *master_f32, uint16_t *prev_bf16, uint64_t 
  *   d = lr * lr_scale * weight_decay
  * m and v are reproducible bit for bit (no fused multiply-add); the quotient
  * and the square root in w may be off by a few units in the last place of the
- * update, and a v below 2^-126 counts as 0 under the root. A grad_scale that is not finite leaves w, m and v as they are (the
- * step of a step's non-finite gradients is skipped without a host round trip).
+ * update, and a v below 2^-126 counts as 0 under the root. A grad_scale that is
+ * not finite leaves w, m and v as they are (a step with non-finite gradients is
+ * skipped without a host round trip).
  *
  * 8-bit moments. Blocks of 256 consecutive elements of a tensor (the last may
  * be shorter) share one exponent byte per moment. With E the FP32 exponent
@@ -823,8 +824,9 @@ int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
  * where the norm is not finite, so that a step given clip_out as grad_scale is
  * skipped. Squares are summed in FP32 over 32 elements and in pairs of FP32
  * numbers (about 48 bits) from there on, in an order that depends on the sizes,
- * alignments and the device alone: the same gradients give the same bits. A sum of squares
- * past FP32's range (gradients above about 1e18) gives a norm that is not finite.
+ * alignments and the device alone: the same gradients give the same bits. A sum
+ * of squares past FP32's range (gradients above about 1e18) gives a norm that is
+ * not finite.
  *   norm_out, clip_out  device, one float each; clip_out may be NULL
  *   max_norm            >= 0 (infinity: never clips)
  */

@@ -751,7 +751,7 @@ void logits_cut(LogitsArgs& a, int sms) {
   a.slices = (a.vocab + a.slice - 1) / a.slice;
 }
 
-// Sorting costs a launch and some 6 ns a token and saves a slice the tokens of the
+// Sorting costs a launch and 6 us a million tokens and saves a slice the tokens of the
 // others, but adds a wait (offsets, then entries), so it needs many tokens and several
 // waves of slices. What the rows read of the token list is known on the device only;
 // two bounds stand for it: the list read once by each slice, and, for a list that rows
