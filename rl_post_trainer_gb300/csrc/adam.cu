@@ -81,7 +81,7 @@ __device__ __forceinline__ void st_f8(float* p, const F8& r) {
 // 8 consecutive gradients from element i on.
 __device__ __forceinline__ F8 ld_grad8(const AdamTensorDesc& d, uint64_t i) {
   if (!d.grad_bf16) return ld_f8(static_cast<const float*>(d.g) + i);
-  const uint4 b = ld_stream_u4_ro(static_cast<const uint16_t*>(d.g) + i);
+  const uint4 b = ld_u4_no_l1(static_cast<const uint16_t*>(d.g) + i);
   F8 r;
   const uint32_t u[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -102,6 +102,7 @@ __device__ __forceinline__ F8 ld_grad8(const AdamTensorDesc& d, uint64_t i) {
 constexpr int kAdam32Ctas = 4;  // CTAs per SM: 64 registers a thread
 __global__ void __launch_bounds__(kAdamThreads, kAdam32Ctas)
     adam32_kernel(const __grid_constant__ AdamLaunch a) {
+  stream_ready();
   const AdamTensorDesc d = a.tensors[a.tile_tensor[blockIdx.x]];
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
   if (d.g == nullptr || !isfinite(scale)) return;
@@ -299,7 +300,7 @@ __device__ __forceinline__ void load_block8(Block8<BF16>& b, const Adam8Ptrs& p,
   }
   b.w = ld_f8(p.w + i);
   if (BF16) {
-    const uint4 u = ld_stream_u4_ro(static_cast<const uint16_t*>(p.g) + i);
+    const uint4 u = ld_u4_no_l1(static_cast<const uint16_t*>(p.g) + i);
     b.g[0] = __uint_as_float(u.x), b.g[1] = __uint_as_float(u.y);
     b.g[2] = __uint_as_float(u.z), b.g[3] = __uint_as_float(u.w);
   } else {
@@ -473,6 +474,7 @@ __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptr
 // element take 169 us (503 when each lane's elements were 32 apart).
 template <bool MIXED>
 __global__ void __launch_bounds__(kAdamThreads, kAdam8Ctas) adam8_kernel(const __grid_constant__ AdamLaunch a) {
+  stream_ready();
   const AdamTensorDesc* const desc = a.tensors + a.tile_tensor[blockIdx.x];
   const AdamTensorDesc d = *desc;
   Adam8Ptrs p{d.w, d.g, static_cast<uint8_t*>(d.m), static_cast<uint8_t*>(d.v), d.m_exp, d.v_exp,
@@ -503,6 +505,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdam8Ctas) adam8_kernel(const _
 // written, bound by memory. 1.54 billion parameters: 2.23 ms, 6.95 TB/s.
 __global__ void __launch_bounds__(kAdamThreads)
     adam_export_kernel(const AdamTensorDesc* tensors, const uint32_t* tile_tensor, uint32_t tile) {
+  stream_ready();
   const AdamTensorDesc& d = tensors[tile_tensor[blockIdx.x]];
   const uint64_t base = (blockIdx.x - d.tile_begin) * tile, n = d.n;
   const uint32_t len = uint32_t(min(n - base, uint64_t(tile)));
@@ -594,7 +597,7 @@ __device__ __forceinline__ Sum2 sum_squares(const void* g, uint64_t lo, uint64_t
       if (q < groups) {
         const char* s = p + (first + 8u * q) * kBytes;
         if (BF16) {
-          const uint4 u = ld_stream_u4_ro(s);
+          const uint4 u = ld_u4_no_l1(s);
           const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -649,6 +652,7 @@ __global__ void __launch_bounds__(kAdamThreads, kNormCtas)
                      float* norm_out, float* clip_out) {
   __shared__ Sum2 smem[kAdamThreads / 32];
   __shared__ bool last;
+  stream_ready();
   Sum2 sum{0.0f, 0.0f};
   for (uint64_t piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
     const uint64_t hi = total_tiles * (piece + 1) / pieces;
@@ -697,22 +701,17 @@ uint32_t adam_key(uint64_t seed, uint64_t step) {
 }
 
 cudaError_t launch_adam32(const AdamLaunch& a, cudaStream_t stream) {
-  adam32_kernel<<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(adam32_kernel, dim3(unsigned(a.total_tiles)), kAdamThreads, stream, a);
 }
 
 cudaError_t launch_adam8(const AdamLaunch& a, cudaStream_t stream) {
-  if (a.mixed)
-    adam8_kernel<true><<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
-  else
-    adam8_kernel<false><<<unsigned(a.total_tiles), kAdamThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(a.mixed ? adam8_kernel<true> : adam8_kernel<false>, dim3(unsigned(a.total_tiles)), kAdamThreads,
+                      stream, a);
 }
 
 cudaError_t launch_adam_export(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
                                uint32_t tile, uint64_t total_tiles, cudaStream_t stream) {
-  adam_export_kernel<<<unsigned(total_tiles), kAdamThreads, 0, stream>>>(tensors, tile_tensor, tile);
-  return cudaGetLastError();
+  return launch_early(adam_export_kernel, dim3(unsigned(total_tiles)), kAdamThreads, stream, tensors, tile_tensor, tile);
 }
 
 cudaError_t launch_grad_norm(const AdamTensorDesc* tensors, const uint32_t* tile_tensor,
@@ -723,9 +722,8 @@ cudaError_t launch_grad_norm(const AdamTensorDesc* tensors, const uint32_t* tile
   if (grid > total_tiles) grid = total_tiles ? total_tiles : 1;
   const uint64_t turn = grid * (kNormPiece / tile);
   const uint64_t pieces = grid * ((total_tiles + turn - 1) / turn);
-  grad_norm_kernel<<<unsigned(grid), kAdamThreads, 0, stream>>>(
-      tensors, tile_tensor, tile, total_tiles, pieces, reinterpret_cast<Sum2*>(partials), ticket, max_norm, norm_out, clip_out);
-  return cudaGetLastError();
+  return launch_early(grad_norm_kernel, dim3(unsigned(grid)), kAdamThreads, stream, tensors, tile_tensor, tile,
+                      total_tiles, pieces, reinterpret_cast<Sum2*>(partials), ticket, max_norm, norm_out, clip_out);
 }
 
 }  // namespace pulse

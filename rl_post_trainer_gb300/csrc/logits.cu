@@ -209,10 +209,10 @@ __device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s,
   const int4* quad = reinterpret_cast<const int4*>(p + lead);
   const int4 none = make_int4(-1, -1, -1, -1);
   uint32_t at = threadIdx.x;
-  int4 next = at < quads ? __ldg(quad + at) : none;
+  int4 next = at < quads ? quad[at] : none;
   for (uint32_t q = threadIdx.x & ~31u; q < quads; q += kThreads, at += kThreads) {
     const int4 t = next;
-    next = at + kThreads < quads ? __ldg(quad + at + kThreads) : none;
+    next = at + kThreads < quads ? quad[at + kThreads] : none;
     four(t, lead + 4u * at, at < quads);
   }
   // up to 3 entries in front of the aligned ones and 3 behind, one a lane of the first warp
@@ -247,7 +247,9 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   __shared__ uint32_t begin[256];
   constexpr int kEach = kBlock / 256;
   const uint64_t base = uint64_t(blockIdx.x) * kBlock;
-  // the kernel that reads the entries may start with what it does before that
+  // the kernel that reads the entries may start with what it does before that; it
+  // counts on what is in front of this one
+  stream_ready();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   count[threadIdx.x] = 0u;
   uint32_t token[kEach], bucket[kEach], place[kEach] = {};
@@ -287,10 +289,6 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   for (int k = 0; k < kEach; ++k)
     entries[base + begin[bucket[k]] + place[k]] = token[k] | ((threadIdx.x + 256u * k) << 16);
 }
-
-// Waits for the sorting in front of this kernel, if there is one. Everything that a
-// call writes is written after it.
-__device__ __forceinline__ void sorted_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // As scan_tokens, of sorted tokens.
 template <typename F>
@@ -459,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
   if (s.row >= a.rows) return;
+  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
   Groups<TIn> g;
   g.load(s, src);
   read_row(a, s.row, history, row);
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  sorted_ready();
+  if (a.sorted) stream_ready();
   if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
@@ -524,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && (a.repetition || a.presence || a.frequency);
   if (s.row >= a.rows) return;
+  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
   Groups<TIn> g;
   g.load(s, src);
   read_row(a, s.row, history, row);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
     return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(made))), pres);
   };
   auto seen = [&](uint32_t u) { return (used[u >> 5] >> (u & 31u)) & 1u; };
-  sorted_ready();
+  if (a.sorted) stream_ready();
   if (row.history) {
     scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
@@ -658,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(cons
   Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
   if (s.row >= a.rows) return;
+  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
   const TIn* raw = static_cast<const TIn*>(a.raw) + (a.raw ? s.row * a.raw_stride : 0u);
   if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
   Groups<TOut> g;
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(cons
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  sorted_ready();
+  if (a.sorted) stream_ready();
   if (row.history) mark_history(a, s, row, bits, raw + int64_t(s.base) - 8);
   mask_ready();
   __syncthreads();
@@ -716,19 +717,9 @@ dim3 grid_of(const LogitsArgs& a) {
   return dim3(a.slices, unsigned(a.rows < kRowsY ? a.rows : kRowsY), unsigned((a.rows + kRowsY - 1) / kRowsY));
 }
 
-// Behind the sorting of its tokens the kernel may start early (sorted_ready).
 template <typename K>
 cudaError_t launch(K kernel, const LogitsArgs& a, cudaStream_t stream) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid_of(a);
-  c.blockDim = dim3(kThreads);
-  c.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = a.sorted ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, a);
+  return launch_early(kernel, grid_of(a), kThreads, stream, a);
 }
 
 }  // namespace
@@ -771,9 +762,8 @@ uint64_t logits_sort_entries(const LogitsArgs& a) { return logits_sort_blocks(a)
 uint64_t logits_sort_offs(const LogitsArgs& a) { return logits_sort_blocks(a) * (a.slices + 2); }
 
 cudaError_t launch_logits_sort(const LogitsArgs& a, uint32_t* entries, uint16_t* offs, cudaStream_t stream) {
-  sort_kernel<<<unsigned(logits_sort_blocks(a)), 256, 0, stream>>>(a.tokens, uint64_t(a.ntokens), a.vocab, a.slice,
-                                                                   a.slices, entries, offs);
-  return cudaGetLastError();
+  return launch_early(sort_kernel, dim3(unsigned(logits_sort_blocks(a))), 256, stream, a.tokens, uint64_t(a.ntokens),
+                      a.vocab, a.slice, a.slices, entries, offs);
 }
 
 cudaError_t launch_logits_shape(const LogitsArgs& a, int in_type, int out_type, cudaStream_t stream) {

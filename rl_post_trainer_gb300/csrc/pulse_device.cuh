@@ -255,6 +255,20 @@ __device__ __forceinline__ uint2 ld_u2_no_l1(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_u4_no_l1(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// In a kernel started by launch_early(): waits for the kernel in front of it in the
+// stream and its writes. Nothing that a stream's work can change is read before this,
+// nothing is written, and nothing read after it goes through the read-only path.
+__device__ __forceinline__ void stream_ready() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t lanemask_lt() {
   uint32_t m;
   asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
