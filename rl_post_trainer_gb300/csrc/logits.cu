@@ -447,7 +447,7 @@ constexpr float kClosed = -__builtin_huge_valf();
 // Repetition penalty and temperature alone: a bit a token is all there is to keep.
 //   y = (seen ? x * (x > 0 ? 1/r : r) : x) * (1/T), -inf where the mask is closed
 // Bound by memory where rows are many: 3,001 FP32 rows of 32,003 with up to 3,001
-// tokens before each take 117 us, 6.6 TB/s.
+// tokens before each take 113 us, 6.8 TB/s.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __grid_constant__ LogitsArgs a) {
   __shared__ uint32_t bits[kWords], open[kWords];
@@ -504,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
 //   y = (p(x) - f * n - (n > 0 ? presence : 0) + b) * (1/T), p(x) as above, n the times
 //   that the token was generated, -inf where the mask is closed
 // A word a place is zeroed for all logits and read for groups of 8 with a token that a
-// list names (1,024 rows with up to 64 tokens each: 95 us, 103 when all were read).
+// list names (1,024 rows with up to 64 tokens each: 93 us, 8 more when all were read).
 // Zeroing the named ones alone took a second pass over the history and a third barrier,
 // and was slower everywhere. Instructions and the waits between the barriers bound this
 // kernel (issue slots 47 %, DRAM 21 %): 256 BF16 rows of 128,256 with histories up to
-// 8,192, 100 biases and half of the rows masked take 53 us, 29 us with up to 64 tokens
+// 8,192, 100 biases and half of the rows masked take 51 us, 27 us with up to 64 tokens
 // and neither biases nor masks, where the logits alone would move in 20.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __grid_constant__ LogitsArgs a) {
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   // A bias list of at most an entry a thread is read here, with the logit and the
   // value that an entry in the slice needs; bits in `final` claim its tokens. A token
   // listed twice is met there and sends the whole list the slow way, which longer
-  // lists go anyhow. (256 rows of 151,936 with up to 256 biases each: 59 us when every
+  // lists go anyhow. (256 rows of 128,256 with 100 biases each: 59 us when every
   // list went the slow way, 54 us so, 56 us with two entries a thread.)
   const uint32_t biased = row.biased, len = s.stop - s.first, off = s.first - s.base + 8u;
   const bool quick = biased <= uint32_t(kThreads);
@@ -646,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
 // Backward: a bit a token of the history, and the raw logits of groups that have one.
 //   dx = open ? dy * (1/T) * (seen ? (x > 0 ? 1/r : r) : 1) : 0
 // (counts and biases are added, so they leave the gradient alone). Raw logits are read
-// only where a token was seen, asked for while it is marked (465 against 458 us).
-// 4,096 BF16 rows of 151,936 with up to 4,096 tokens before each: 458 us, 5.5 TB/s;
+// only where a token was seen, asked for while it is marked (7 us less in the case below).
+// 4,096 BF16 rows of 151,936 with up to 4,096 tokens before each: 455 us, 5.5 TB/s;
 // 376 us, 6.7 TB/s, with 64 tokens, so what bounds it is the waits for the history.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(const __grid_constant__ LogitsArgs a) {
