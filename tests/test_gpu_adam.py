@@ -388,6 +388,36 @@ def test_clipped_step_end_to_end():
 
 # ------------------------------------------------------------------ refusals
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", [[300, 7, 70001], [1 << 20], [2000003, 4096, 400000]])
+def test_calls_back_to_back(bits, sizes):
+    """Kernels start while the one in front of them ends: the bits are those of calls with a wait after each."""
+    _cuda()
+    results = []
+    for wait in (True, False):
+        model = Model(sizes, bits, seed=5)
+        grads = [p["buf"]["g"].t for p in model.parts]
+        seen = []
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        for t in range(1, 41):
+            for g in grads:
+                g.mul_(-0.9).add_(1e-4)
+            pause()
+            norm, clip = model.plan.grad_norm(0.1)
+            pause()
+            model.plan.step(t, LR, B1, B2, EPS, grad_scale=clip, seed=t)
+            pause()
+            if bits == 8:
+                model.plan.export_states()
+                pause()
+            seen += [norm, clip, model.parts[0]["buf"]["w"].t.sum(), model.parts[-1]["buf"]["w"].t.sum()]
+            pause()
+        torch.cuda.synchronize()
+        names = ("w", "m", "v") + (("m_exp", "v_exp", "m_out", "v_out") if bits == 8 else ())
+        results.append([x.clone() for x in seen] + [p["buf"][k].t.clone() for p in model.parts for k in names])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_refusals():
     dev = _cuda()
     f = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731

@@ -502,6 +502,40 @@ def test_sorted_and_captured_calls_agree():
     assert torch.equal(out, want) and torch.equal(dx, back)
 
 
+@pytest.mark.parametrize("rows,vocab,history", [(3, 5003, 60), (64, 32003, 500), (12, WIDE, 60000)])
+def test_calls_back_to_back(rows, vocab, history):
+    """Kernels start while the one in front of them ends: the bits are those of calls with a wait after each."""
+    _cuda()
+    s = settings(rows, vocab, history=history, seed=34)
+    plan = plan_of(s, rows, vocab)
+    tokens, bias = plan.tensors["tokens"], plan.tensors["bias_values"]
+    first, first_bias = tokens.clone(), bias.clone()
+    results = []
+    for wait in (True, False):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        tokens.copy_(first), bias.copy_(first_bias)
+        x = torch.randn(rows, vocab, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+        d, y, dx = (torch.zeros_like(x) for _ in range(3))
+        seen = []
+        for _ in range(20):
+            x.mul_(0.9).add_(0.1)  # written by the kernel in front, as are the tokens and the biases
+            tokens.add_(1).remainder_(vocab)
+            bias.neg_()
+            pause()
+            plan.shape(x, out=y)
+            pause()
+            d.copy_(y).clamp_(-3, 3)
+            pause()
+            plan.backward(d, logits=x, out=dx)
+            pause()
+            x.add_(dx, alpha=0.01)  # read by the one behind
+            seen.append(x[:, :: max(1, vocab // 997)].clone())
+            pause()
+        torch.cuda.synchronize()
+        results.append(seen + [y.clone(), dx.clone()])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_on_another_stream():
     _cuda()
     rows, vocab = 16, 20011
