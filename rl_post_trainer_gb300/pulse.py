@@ -1213,33 +1213,25 @@ ADAM_BLOCK = 256
 _F32_BF16 = (torch.float32, torch.bfloat16)
 
 
-def _type_code(t: torch.Tensor) -> int:
-    return 1 if t.dtype == torch.bfloat16 else 0
+_TYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}
 
 
-class _on_device:
-    """``dev`` as the current CUDA device inside a with block; no CUDA call
-    where it already is."""
-
-    __slots__ = ("index", "back")
-
-    def __init__(self, dev: torch.device):
-        self.index, self.back = dev.index, None
-
-    def __enter__(self):
-        now = torch._C._cuda_getDevice()
-        if now != self.index:
-            self.back = now
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
-
-
-def _raw_stream(dev: torch.device) -> int:
-    """torch's current stream of ``dev`` as a number, without building a Stream."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _call(name: str, dev: torch.device, *args):
+    """The entry point ``name`` with ``dev`` as the current CUDA device and torch's
+    current stream there as its last argument. No CUDA call where ``dev`` is current
+    already, no Stream object: small calls take as long as this."""
+    fn = getattr(lib(), name)
+    now = torch._C._cuda_getDevice()
+    if now == dev.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(now))
+    else:
+        torch.cuda.set_device(dev.index)
+        try:
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        finally:
+            torch.cuda.set_device(now)
+    if st != PULSE_OK:
+        raise PulseError(st, name)
 
 
 def _indexed(dev: torch.device) -> torch.device:
@@ -1330,9 +1322,7 @@ class AdamPlan:
             if g is not None:
                 _need(g, "grad", (s.grad_dtype,), self.device, s.n)
                 arr[i] = g.data_ptr()
-        with _on_device(self.device):
-            st = lib().pulse_adam_plan_set_grads(self._h, arr, _raw_stream(self.device))
-        _raise(st, "pulse_adam_plan_set_grads")
+        _call("pulse_adam_plan_set_grads", self.device, self._h, arr)
         for s, g in zip(self.slots, grads):
             s.grad = g
 
@@ -1349,10 +1339,7 @@ class AdamPlan:
             clip_out = torch.empty(1, dtype=torch.float32, device=self.device)
         else:
             _need(clip_out, "clip_out", (torch.float32,), self.device, min_numel=1)
-        with _on_device(self.device):
-            st = lib().pulse_grad_norm_multi(self._h, max_norm, norm_out.data_ptr(),
-                                             clip_out.data_ptr(), _raw_stream(self.device))
-        _raise(st, "pulse_grad_norm_multi")
+        _call("pulse_grad_norm_multi", self.device, self._h, max_norm, norm_out.data_ptr(), clip_out.data_ptr())
         return norm_out, clip_out
 
     def step(self, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -1367,15 +1354,11 @@ class AdamPlan:
             _need(grad_scale, "grad_scale", (torch.float32,), self.device, min_numel=1)
             scale = grad_scale.data_ptr()
         h = PulseAdamHyper(step, seed & 0xFFFFFFFFFFFFFFFF, lr, beta1, beta2, eps)
-        with _on_device(self.device):
-            st = lib().pulse_adam_step_multi(self._h, ctypes.byref(h), scale, _raw_stream(self.device))
-        _raise(st, "pulse_adam_step_multi")
+        _call("pulse_adam_step_multi", self.device, self._h, ctypes.byref(h), scale)
 
     def export_states(self):
         """8-bit moments as FP32 values into every slot's ``m_out`` and ``v_out``."""
-        with _on_device(self.device):
-            st = lib().pulse_adam_export_multi(self._h, _raw_stream(self.device))
-        _raise(st, "pulse_adam_export_multi")
+        _call("pulse_adam_export_multi", self.device, self._h)
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -1497,10 +1480,8 @@ class LogitsPlan:
             out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
         allowed = _F32_BF16 if logits.dtype == torch.bfloat16 else (torch.float32,)
         dst, out_stride = self._rows_of(out, "out", allowed, logits)
-        with _on_device(self.device):
-            st = lib().pulse_logits_shape(self._ref, logits.shape[0], src, stride, _type_code(logits),
-                                          dst, out_stride, _type_code(out), _raw_stream(self.device))
-        _raise(st, "pulse_logits_shape")
+        _call("pulse_logits_shape", self.device, self._ref, logits.shape[0], src, stride, _TYPE_CODE[logits.dtype],
+              dst, out_stride, _TYPE_CODE[out.dtype])
         return out
 
     def backward(self, dout: torch.Tensor, logits: Optional[torch.Tensor] = None,
@@ -1521,9 +1502,6 @@ class LogitsPlan:
         if out is None:
             out = torch.empty(dout.shape, dtype=in_dtype, device=dout.device)
         dst, out_stride = self._rows_of(out, "out", (in_dtype,), dout)
-        with _on_device(self.device):
-            st = lib().pulse_logits_shape_backward(
-                self._ref, dout.shape[0], d, d_stride, _type_code(dout), raw, raw_stride,
-                1 if in_dtype == torch.bfloat16 else 0, dst, out_stride, _raw_stream(self.device))
-        _raise(st, "pulse_logits_shape_backward")
+        _call("pulse_logits_shape_backward", self.device, self._ref, dout.shape[0], d, d_stride,
+              _TYPE_CODE[dout.dtype], raw, raw_stride, _TYPE_CODE[in_dtype], dst, out_stride)
         return out
