@@ -873,7 +873,8 @@ int pulse_adam_export_multi(pulse_adam_plan *plan, cudaStream_t stream);
  * vocabulary they fall, into a library workspace per (device, stream) of about 4 bytes a token,
  * allocated on first use and grown on demand (growth synchronises `stream`).
  * Nothing of it is kept for the next call. A call that is being captured into a
- * graph, and one without room, works on the tokens as they are. Errors of a stream
+ * graph, one on cudaStreamPerThread, and one without room, works on the tokens as they
+ * are. Host threads may call on one stream at the same time. Errors of a stream
  * that made its first call in a capture are reported by pulse_get_error of every
  * stream.
  * ---------------------------------------------------------------------- */

@@ -1781,6 +1781,8 @@ bool rows_ok(const RowsOf& r, uint64_t vocab) {
 }
 
 // Sorted histories of one stream (kernels on it run in order, so calls share it).
+// Whoever fills them holds g_ws_mu until the kernel that reads them is enqueued: calls
+// of other host threads on the same stream come before the sorting or after that kernel.
 struct LogitsWorkspace {
   uint32_t* entries = nullptr;
   uint16_t* offs = nullptr;
@@ -1815,7 +1817,9 @@ bool logits_reserve(LogitsWorkspace& w, uint64_t entries, uint64_t offs, cudaStr
 }
 
 // Fills the shaping's part and the stream's error word, and sorts the tokens
-// where `history` is read and the sorting pays.
+// where `history` is read and the sorting pays. The caller holds g_ws_mu until it
+// has launched the kernel that takes *a. The handle of the per-thread default stream
+// names another stream in every thread, so calls on it share no sorted histories.
 int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cudaStream_t stream,
                 LogitsArgs* a) {
   // one CTA per slice of a row: rows fit the grid's second and third dimension
@@ -1843,7 +1847,6 @@ int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cuda
   a->mask_row = s.mask_row;
   const int sms = sm_count(device);
   logits_cut(*a, sms);
-  std::lock_guard<std::mutex> lock(g_ws_mu);
   try {
     Workspace* ws = stream_workspace(device, stream);
     if (ws == nullptr) return PULSE_ERR_NOMEM;
@@ -1856,7 +1859,8 @@ int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cuda
     if (st != PULSE_OK) return st;
     a->error_word = ws->counters + 2;
     // a captured call may be replayed when the workspace has grown or is in use
-    if (!history || !logits_sorts(*a, sms) || stream_captured(stream)) return PULSE_OK;
+    if (!history || stream == cudaStreamPerThread || !logits_sorts(*a, sms) || stream_captured(stream))
+      return PULSE_OK;
     LogitsWorkspace*& lw = g_logits_ws[std::make_pair(device, reinterpret_cast<uintptr_t>(stream))];
     if (lw == nullptr) lw = new (std::nothrow) LogitsWorkspace();
     if (lw == nullptr) return PULSE_ERR_NOMEM;
@@ -1882,6 +1886,7 @@ int pulse_logits_shape(const pulse_logits_shaping* shaping, uint64_t rows, const
   if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
   LogitsArgs a{};
   const bool history = shaping->tokens && (shaping->repetition || shaping->presence || shaping->frequency);
+  std::lock_guard<std::mutex> lock(g_ws_mu);
   const int st = logits_args(*shaping, rows, history, stream, &a);
   if (st != PULSE_OK) return st;
   a.src = logits;
@@ -1906,6 +1911,7 @@ int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t ro
     return PULSE_ERR_INVALID;
   if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
   LogitsArgs a{};
+  std::lock_guard<std::mutex> lock(g_ws_mu);
   const int st = logits_args(*shaping, rows, needs_raw, stream, &a);
   if (st != PULSE_OK) return st;
   a.src = dout;
