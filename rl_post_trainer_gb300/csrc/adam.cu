@@ -486,7 +486,10 @@ __global__ void __launch_bounds__(kAdamThreads, kAdam8Ctas) adam8_kernel(const _
   const uint32_t per_warp = a.tile / kAdamBlock / (kAdamThreads / 32);
   const uint64_t first = (blockIdx.x - d.tile_begin) * (a.tile / kAdamBlock) +
                          (threadIdx.x >> 5) * per_warp;
-  const uint64_t whole = MIXED && lead == kAdamNoGroups ? 0u : n / kAdamBlock;  // blocks that take the short way
+  // Blocks that take the short way. A graph keeps the kernel that its plan had when it was
+  // captured, while the tensors it reads may since have new gradients: the kernel for
+  // aligned plans looks at `lead` too, and takes the general way where it is not 0.
+  const uint64_t whole = lead == 0u || (MIXED && lead == kAdamCodeGroups) ? n / kAdamBlock : 0u;
   uint32_t done = 0;
   if (first < whole) {
     done = uint32_t(min(whole - first, uint64_t(per_warp)));

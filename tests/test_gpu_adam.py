@@ -458,3 +458,50 @@ def test_refusals():
     half = pulse.AdamPlan([S(8, f(8), f(8), f(8, torch.uint8), f(8, torch.uint8))], state_bits=8)
     with pytest.raises(pulse.PulseError):
         half.step(1, 1e-3)
+
+
+# ------------------------------------------- gradients that move under a plan
+
+def _new_grads(model, shift, seed):
+    """Gradients for every tensor of the model, `shift` elements into their buffers."""
+    gen = torch.Generator().manual_seed(seed)
+    for p in model.parts:
+        old = p["buf"]["g"].t
+        g = (torch.randn(p["n"], generator=gen) * 1e-3).to(old.dtype)
+        p["buf"]["g"], p["g"] = Shifted(g, old.dtype, shift), g.float().numpy()
+    model.plan.set_grads([p["buf"]["g"].t for p in model.parts])
+
+
+class Replayed:
+    """A plan whose step is the replay of one captured step: its number, rate and seed stay."""
+
+    def __init__(self, plan, t, seed):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        self.plan, self.graph, self.args = plan, torch.cuda.CUDAGraph(), (t, seed)
+        with torch.cuda.stream(side), torch.cuda.graph(self.graph, stream=side):
+            plan.step(t, LR, B1, B2, EPS, seed=seed)
+        torch.cuda.current_stream().wait_stream(side)
+
+    def step(self, t, lr, b1, b2, eps, grad_scale, seed):
+        assert (t, seed) == self.args and grad_scale is None
+        self.graph.replay()
+
+    def set_grads(self, grads):
+        self.plan.set_grads(grads)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("shifts", [(0, 1, 0, 4), (3, 0, 8, 2)])
+def test_new_gradients_of_another_alignment(bits, grad, captured, shifts):
+    """Gradients on their groups and off them in turn, also under a step that was captured with others."""
+    _cuda()
+    model = Model([70001, 256, 0, 5000, 8192], bits, grad, 0, seed=21)
+    for k, shift in enumerate(shifts):
+        _new_grads(model, shift, 100 + k)
+        if captured and k == 0:
+            model.plan = Replayed(model.plan, 5, 77)
+        model.step(5, seed=77)
+        model.check()
