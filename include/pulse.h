@@ -814,7 +814,8 @@ int pulse_adam_plan_destroy(pulse_adam_plan *plan); /* synchronises the device; 
 
 /* New gradient pointers (host array of ntensors device pointers, NULL entries
  * as in the plan; the types stay), copied before the call returns and used by
- * work that is enqueued on `stream` after it. Not while `stream` is being captured. */
+ * work that is enqueued on `stream` after it, replays of captured steps included.
+ * PULSE_ERR_INVALID while `stream` is being captured. Where a call fails the plan stays as it was. */
 int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
                               cudaStream_t stream);
 

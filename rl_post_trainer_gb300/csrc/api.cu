@@ -1519,6 +1519,11 @@ int pulse_mx_plan_get_error(pulse_mx_plan* plan) {
 
 namespace {
 
+bool stream_captured(cudaStream_t stream) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  return cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
+}
+
 bool grad_pointer_ok(const void* g, int type) { return aligned(g, type == PULSE_BF16 ? 2 : 4); }
 
 bool adam_tensor_ok(const pulse_adam_tensor& t, int state_bits) {
@@ -1672,21 +1677,27 @@ int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, c
   for (int i = 0; i < plan->ntensors; ++i)
     if (!grad_pointer_ok(grads[i], plan->host_desc[size_t(i)].grad_bf16 ? PULSE_BF16 : PULSE_F32))
       return PULSE_ERR_INVALID;
+  // a captured copy would read the staging buffer when the graph runs, whatever it holds then
+  if (stream_captured(stream)) return PULSE_ERR_INVALID;
   const size_t bytes = sizeof(AdamTensorDesc) * plan->host_desc.size();
   if (plan->staged == nullptr && cudaEventCreateWithFlags(&plan->staged, cudaEventDisableTiming) != cudaSuccess)
     return PULSE_ERR_CUDA;
   if (plan->staging == nullptr && cudaMallocHost(&plan->staging, bytes) != cudaSuccess) return PULSE_ERR_NOMEM;
-  for (int i = 0; i < plan->ntensors; ++i) {
-    AdamTensorDesc& d = plan->host_desc[size_t(i)];
-    d.g = grads[i];
-    d.lead = adam_lead(d, plan->state_bits);
-  }
-  plan->mixed = adam_mixed(plan->host_desc);
   // the copy before this one has left the pinned buffer
   if (cudaEventSynchronize(plan->staged) != cudaSuccess) return PULSE_ERR_CUDA;
   std::memcpy(plan->staging, plan->host_desc.data(), bytes);
+  bool mixed = false;
+  for (int i = 0; i < plan->ntensors; ++i) {
+    AdamTensorDesc& d = plan->staging[i];
+    d.g = grads[i];
+    d.lead = adam_lead(d, plan->state_bits);
+    mixed = mixed || (d.lead != 0 && d.n > 0);
+  }
   if (cudaMemcpyAsync(plan->desc, plan->staging, bytes, cudaMemcpyHostToDevice, stream) != cudaSuccess)
     return PULSE_ERR_CUDA;
+  // from here on the device has the new gradients; up to here the plan is as it was
+  std::memcpy(plan->host_desc.data(), plan->staging, bytes);
+  plan->mixed = mixed;
   return cuda_status(cudaEventRecord(plan->staged, stream));
 }
 
@@ -1789,11 +1800,6 @@ struct LogitsWorkspace {
   uint64_t entry_cap = 0, offs_cap = 0;
 };
 std::map<std::pair<int, uintptr_t>, LogitsWorkspace*> g_logits_ws;
-
-bool stream_captured(cudaStream_t stream) {
-  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  return cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
-}
 
 // Room for a call's sorted histories; growth synchronises `stream`. Returns false
 // where there is no memory for it: the call then works on the unsorted tokens.

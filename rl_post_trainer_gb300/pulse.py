@@ -1314,7 +1314,8 @@ class AdamPlan:
         self._h = handle
 
     def set_grads(self, grads: Sequence[Optional[torch.Tensor]]):
-        """New gradient tensors (None: no gradient), of the types and sizes the plan has."""
+        """New gradient tensors (None: no gradient), of the types and sizes the plan has.
+        Not inside a stream capture; replays of steps captured before see them."""
         if len(grads) != self.ntensors:
             raise ValueError(f"{len(grads)} gradients, the plan has {self.ntensors} tensors")
         arr = (ctypes.c_void_p * self.ntensors)()

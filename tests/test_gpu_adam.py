@@ -505,3 +505,26 @@ def test_new_gradients_of_another_alignment(bits, grad, captured, shifts):
             model.plan = Replayed(model.plan, 5, 77)
         model.step(5, seed=77)
         model.check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_new_gradients_in_a_capture_are_refused(bits):
+    """The capture goes on, and the plan keeps the gradients it had."""
+    _cuda()
+    model = Model([3001, 40], bits, seed=22)
+    other = [torch.ones(p["n"] + 1, device="cuda")[1:] for p in model.parts]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for k in range(2):  # without and with a staging buffer
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+            with pytest.raises(pulse.PulseError):
+                model.plan.set_grads(other)
+            norm, clip = model.plan.grad_norm(1e30)
+        torch.cuda.current_stream().wait_stream(side)
+        graph.replay()
+        want = np.sqrt(sum(float(np.square(p["g"].astype(np.float64)).sum()) for p in model.parts))
+        assert abs(norm.item() - want) <= want * NORM_TOL and clip.item() == 1.0
+        model.step(1 + k, seed=3)
+        model.check()
+        _new_grads(model, 1, 50 + k)
