@@ -235,8 +235,9 @@ __device__ __forceinline__ void scan_tokens(const LogitsArgs& a, const Slice& s,
 // most of the work. With enough of it the token list is therefore sorted first:
 // block by block of kBlock tokens, the tokens of one slice side by side. A slice
 // then reads its own part of the blocks its history touches. The sorting of 1.3
-// million tokens takes 8 us, its waits one after the other, part of it under the
-// start of the next kernel.
+// million tokens takes 8 us, its waits one after the other. The next kernel starts
+// under it, but reads nothing before its own wait: that the sorting has waited for
+// what is in front of it makes those writes visible to the sorting alone.
 // entries: place in the slice's vocabulary | position in the block << 16; offs:
 // for every block, where each slice's entries begin (slices + 2 words; the slice
 // past the last holds tokens outside the vocabulary).
@@ -247,8 +248,7 @@ __global__ void __launch_bounds__(256) sort_kernel(const int32_t* tokens, uint64
   __shared__ uint32_t begin[256];
   constexpr int kEach = kBlock / 256;
   const uint64_t base = uint64_t(blockIdx.x) * kBlock;
-  // the kernel that reads the entries may start with what it does before that; it
-  // counts on what is in front of this one
+  // the kernel that reads the entries may start: it clears its tables, then waits
   stream_ready();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   count[threadIdx.x] = 0u;
@@ -457,15 +457,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
   if (s.row >= a.rows) return;
-  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  stream_ready();
   Groups<TIn> g;
   g.load(s, src);
   read_row(a, s.row, history, row);
-  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  if (a.sorted) stream_ready();
   if (row.history) mark_history(a, s, row, bits);
   mask_ready();
   __syncthreads();
@@ -523,14 +522,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
   const Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && (a.repetition || a.presence || a.frequency);
   if (s.row >= a.rows) return;
-  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
-  Groups<TIn> g;
-  g.load(s, src);
-  read_row(a, s.row, history, row);
   if (threadIdx.x == 0) twice = 0u;
   for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) final[i] = used[i] = 0u;
   for (uint32_t i = threadIdx.x; i < (a.slice + 8u + 3u) / 4u; i += kThreads)
     reinterpret_cast<uint4*>(word)[i] = make_uint4(0u, 0u, 0u, 0u);
+  stream_ready();
+  Groups<TIn> g;
+  g.load(s, src);
+  read_row(a, s.row, history, row);
   __syncthreads();
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   const uint32_t* mask = row.mask;
@@ -562,7 +561,6 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __
     return made == 0u ? x : __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(made))), pres);
   };
   auto seen = [&](uint32_t u) { return (used[u >> 5] >> (u & 31u)) & 1u; };
-  if (a.sorted) stream_ready();
   if (row.history) {
     scan_history(a, s, row, [&](const Four& x) {
 #pragma unroll
@@ -658,17 +656,16 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TOut>) backward_kernel(cons
   Slice s = slice_of(a, src, dst);
   const bool history = a.tokens && a.repetition;
   if (s.row >= a.rows) return;
-  if (!a.sorted) stream_ready();  // else the sorting has waited for all but its own results
+  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
+  stream_ready();
   const TIn* raw = static_cast<const TIn*>(a.raw) + (a.raw ? s.row * a.raw_stride : 0u);
   if (a.raw && lead_of(raw) != lead_of(src)) s.grouped = false;  // places stay as they are
   Groups<TOut> g;
   g.load(s, src);
   read_row(a, s.row, history, row);
-  for (uint32_t i = threadIdx.x; i < kWords; i += kThreads) bits[i] = 0u;
   __syncthreads();
   const uint32_t* mask = row.mask;
   copy_mask(mask, s, open);
-  if (a.sorted) stream_ready();
   if (row.history) mark_history(a, s, row, bits, raw + int64_t(s.base) - 8);
   mask_ready();
   __syncthreads();
