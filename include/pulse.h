@@ -906,7 +906,8 @@ typedef struct pulse_logits_shaping {
  * logits itself (same type and stride); any other overlap is refused.
  * A token number outside [0, vocab), a range outside its list or a mask row
  * past mask_rows is left out and recorded as PULSE_ERR_INDEX for
- * pulse_get_error(stream). rows == 0 launches nothing. Errors: PULSE_ERR_INVALID,
+ * pulse_get_error(stream). rows == 0 launches nothing. Errors: PULSE_ERR_INVALID
+ * (also a pointer that is not aligned to its element type),
  * PULSE_ERR_RANGE (rows > 2^30, or too many rows for the vocabulary),
  * PULSE_ERR_NOMEM, PULSE_ERR_CUDA.
  */

@@ -1704,6 +1704,7 @@ int pulse_adam_plan_set_grads(pulse_adam_plan* plan, const void* const* grads, c
 int pulse_grad_norm_multi(pulse_adam_plan* plan, float max_norm, float* norm_out, float* clip_out,
                           cudaStream_t stream) {
   if (plan == nullptr || norm_out == nullptr || !(max_norm >= 0.0f)) return PULSE_ERR_INVALID;
+  if (!aligned(norm_out, 4) || !aligned(clip_out, 4)) return PULSE_ERR_INVALID;
   return cuda_status(launch_grad_norm(plan->desc, plan->tile_tensor, plan->tile, plan->total_tiles,
                                       sm_count(plan->device), plan->partials,
                                       reinterpret_cast<uint32_t*>(plan->partials + kNormMaxCtas),
@@ -1712,7 +1713,8 @@ int pulse_grad_norm_multi(pulse_adam_plan* plan, float max_norm, float* norm_out
 
 int pulse_adam_step_multi(pulse_adam_plan* plan, const pulse_adam_hyper* h, const float* grad_scale,
                           cudaStream_t stream) {
-  if (plan == nullptr || h == nullptr || !plan->can_step || h->step < 1) return PULSE_ERR_INVALID;
+  if (plan == nullptr || h == nullptr || !plan->can_step || h->step < 1 || !aligned(grad_scale, 4))
+    return PULSE_ERR_INVALID;
   if (!(std::isfinite(h->lr) && h->lr >= 0.0) || !(h->beta1 >= 0.0 && h->beta1 < 1.0) ||
       !(h->beta2 >= 0.0 && h->beta2 < 1.0) || !(std::isfinite(h->eps) && h->eps >= 0x1p-126))
     return PULSE_ERR_INVALID;
@@ -1780,6 +1782,14 @@ bool same_rows(const RowsOf& a, const RowsOf& b) {
 
 bool shaping_ok(const pulse_logits_shaping* s) {
   if (s == nullptr || s->vocab < 1 || s->vocab >= (1ull << 31)) return false;
+  for (const void* p : {static_cast<const void*>(s->tokens), static_cast<const void*>(s->repetition),
+                        static_cast<const void*>(s->presence), static_cast<const void*>(s->frequency),
+                        static_cast<const void*>(s->temperature), static_cast<const void*>(s->bias_tokens),
+                        static_cast<const void*>(s->bias_values), static_cast<const void*>(s->mask),
+                        static_cast<const void*>(s->mask_row)})
+    if (!aligned(p, 4)) return false;
+  for (const int64_t* p : {s->begin, s->split, s->end, s->bias_begin})
+    if (!aligned(p, 8)) return false;
   if (s->tokens && (s->begin == nullptr || s->end == nullptr || s->ntokens >= (1ull << 62))) return false;
   if (s->bias_tokens && (s->bias_values == nullptr || s->bias_begin == nullptr || s->nbias >= (1ull << 31)))
     return false;

@@ -137,3 +137,16 @@ def test_binding_refuses_cpu_tensors_and_bad_settings(lib):
     with pytest.raises(TypeError):
         pulse.LogitsPlan(1, 8).backward(x.reshape(1, 8))
     assert pulse.adam_blocks(0) == 0 and pulse.adam_blocks(1) == 1 and pulse.adam_blocks(257) == 2
+
+
+def test_misaligned_settings_are_refused(lib):
+    """Every list is read an element at a time: its pointer has to be aligned to that, used in the call or not."""
+    full = dict(tokens=A, begin=A, split=A, end=A, ntokens=4, repetition=A, presence=A, frequency=A, temperature=A,
+                bias_tokens=A, bias_values=A, bias_begin=A, nbias=4, mask=A, mask_rows=4, mask_stride=4, mask_row=A)
+    for name, step in ((n, 4 if n in ("begin", "split", "end", "bias_begin") else 2) for n in full
+                       if n not in ("ntokens", "nbias", "mask_rows", "mask_stride")):
+        s = shaping(**{**full, name: A + step})
+        assert lib.pulse_logits_shape(s, 4, P(B), 100, 0, P(C), 100, 0, P(0)) == E.PULSE_ERR_INVALID, name
+        assert lib.pulse_logits_shape_backward(s, 4, P(B), 100, 0, P(2 * C), 100, 0, P(C), 100, P(0)) == E.PULSE_ERR_INVALID
+        assert lib.pulse_logits_shape(s, 0, P(B), 100, 0, P(C), 100, 0, P(0)) == E.PULSE_ERR_INVALID, name
+    assert lib.pulse_logits_shape(shaping(**full), 0, P(B), 100, 0, P(C), 100, 0, P(0)) == E.PULSE_OK

@@ -528,3 +528,18 @@ def test_new_gradients_in_a_capture_are_refused(bits):
         model.step(1 + k, seed=3)
         model.check()
         _new_grads(model, 1, 50 + k)
+
+
+def test_misaligned_scalars_are_refused():
+    """On the host, before any kernel sees them."""
+    _cuda()
+    import ctypes
+    plan = Model([300], 32).plan
+    lib, raw = pulse.lib(), torch.zeros(16, dtype=torch.uint8, device="cuda")
+    at, invalid = raw.data_ptr(), pulse.pulse.PULSE_ERR_INVALID
+    h = pulse.pulse.PulseAdamHyper(1, 0, LR, B1, B2, EPS)
+    for off in (1, 2, 3):
+        assert lib.pulse_grad_norm_multi(plan._h, 1.0, at + off, at + 4, None) == invalid
+        assert lib.pulse_grad_norm_multi(plan._h, 1.0, at, at + 4 + off, None) == invalid
+        assert lib.pulse_adam_step_multi(plan._h, ctypes.byref(h), at + off, None) == invalid
+    assert not raw.any()
