@@ -1382,6 +1382,26 @@ class AdamPlan:
 
 # ------------------------------------------------------------- logit shaping
 
+class _Shaped(torch.autograd.Function):
+    """LogitsPlan.shape for logits that require a gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, plan, out_dtype):
+        ctx.plan, ctx.dtype = plan, logits.dtype
+        penalty = bool(plan._c.tokens and plan._c.repetition)
+        # what the gradient reads: autograd refuses a backward pass after one of them was changed in place
+        names = ("temperature", "mask", "mask_row") + (("tokens", "begin", "split", "end", "repetition") if penalty else ())
+        ctx.save_for_backward(logits if penalty else None, *(plan.tensors[k] for k in names))
+        return plan.shape(logits.detach(), out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        logits = ctx.saved_tensors[0]
+        out = torch.empty(dout.shape, dtype=ctx.dtype, device=dout.device)
+        return ctx.plan.backward(dout.contiguous(), logits=logits, out=out), None, None
+
+
 class LogitsPlan:
     """Settings of up to ``rows`` requests (or training positions) for pulse_logits_shape.
 
@@ -1475,7 +1495,15 @@ class LogitsPlan:
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
         """Shaped logits of the first ``logits.shape[0]`` rows. ``out`` may be
         ``logits`` (in place); by default a new tensor of ``out_dtype`` (that of
-        ``logits``). FP32 logits give FP32, BF16 logits BF16 or FP32."""
+        ``logits``). FP32 logits give FP32, BF16 logits BF16 or FP32.
+
+        Differentiable with respect to ``logits`` (not to the settings) where they require a
+        gradient and ``out`` is not given. The settings then have to stay as they are until
+        the backward pass."""
+        if logits.requires_grad and torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("out: the logits require a gradient, which a result in a given buffer does not carry")
+            return _Shaped.apply(logits, self, out_dtype)
         src, stride = self._rows_of(logits, "logits", _F32_BF16)
         if out is None:
             out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
