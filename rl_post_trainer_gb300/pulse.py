@@ -1234,6 +1234,12 @@ def _call(name: str, dev: torch.device, *args):
         raise PulseError(st, name)
 
 
+def _overwritten(t: torch.Tensor):
+    """Tells autograd that an input's values are gone: a backward pass that saved them has to fail."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _indexed(dev: torch.device) -> torch.device:
     """``dev`` with its index (torch.device("cuda") has none)."""
     dev = torch.device(dev)
@@ -1511,6 +1517,8 @@ class LogitsPlan:
         dst, out_stride = self._rows_of(out, "out", allowed, logits)
         _call("pulse_logits_shape", self.device, self._ref, logits.shape[0], src, stride, _TYPE_CODE[logits.dtype],
               dst, out_stride, _TYPE_CODE[out.dtype])
+        if dst == src:
+            _overwritten(out)
         return out
 
     def backward(self, dout: torch.Tensor, logits: Optional[torch.Tensor] = None,
@@ -1533,4 +1541,6 @@ class LogitsPlan:
         dst, out_stride = self._rows_of(out, "out", (in_dtype,), dout)
         _call("pulse_logits_shape_backward", self.device, self._ref, dout.shape[0], d, d_stride,
               _TYPE_CODE[dout.dtype], raw, raw_stride, _TYPE_CODE[in_dtype], dst, out_stride)
+        if dst == d:
+            _overwritten(out)
         return out

@@ -101,3 +101,25 @@ def test_given_buffers_carry_no_gradient():
     y = plan.shape(x.to(BF16), out_dtype=F32)
     y.sum().backward()
     assert torch.equal(x.grad, torch.full_like(x, 2.0))
+
+
+@pytest.mark.parametrize("call", ["shape", "backward"])
+def test_in_place_calls_are_seen_by_autograd(call):
+    """A tensor that a backward pass needs and that a call changed in place makes that pass fail."""
+    _cuda()
+    plan = plan_of(dict(NONE, temperature=np.full(2, 0.5, np.float32)), 2, 64)
+    run = plan.shape if call == "shape" else plan.backward
+    w = torch.ones(2, 64, device="cuda", requires_grad=True)
+    for in_place in (False, True):
+        x = torch.randn(2, 64, device="cuda")
+        y = (w * x).sum()
+        run(x, out=x if in_place else torch.empty_like(x))
+        if in_place:
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward()
+        else:
+            y.backward()
+    with torch.inference_mode():
+        x = torch.randn(2, 64, device="cuda")
+        want = x * 2
+        assert torch.equal(run(x, out=x), want)
