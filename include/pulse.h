@@ -827,7 +827,9 @@ int pulse_adam_plan_set_grads(pulse_adam_plan *plan, const void *const *grads,
  * numbers (about 48 bits) from there on, in an order that depends on the sizes,
  * alignments and the device alone: the same gradients give the same bits. A sum
  * of squares past FP32's range (gradients above about 1e18) gives a norm that is
- * not finite.
+ * not finite. At the other end a square below 2^-126 (a gradient below about 1e-19)
+ * is rounded to a multiple of 2^-149, so gradients below 2^-75 (2.6e-23) count as 0:
+ * gradients of that size throughout need scaling first.
  *   norm_out, clip_out  device, one float each; clip_out may be NULL
  *   max_norm            >= 0 (infinity: never clips)
  */

@@ -1337,7 +1337,8 @@ class AdamPlan:
                   clip_out: Optional[torch.Tensor] = None):
         """(norm, clip): one-element FP32 tensors on the device. ``clip`` is the
         factor that brings the norm down to ``max_norm``, NaN for a norm that is
-        not finite; ``step(grad_scale=clip)`` applies it, and skips on NaN."""
+        not finite; ``step(grad_scale=clip)`` applies it, and skips on NaN. Gradients
+        below 2^-75 count as 0."""
         if norm_out is None:
             norm_out = torch.empty(1, dtype=torch.float32, device=self.device)
         else:

@@ -543,3 +543,29 @@ def test_misaligned_scalars_are_refused():
         assert lib.pulse_grad_norm_multi(plan._h, 1.0, at, at + 4 + off, None) == invalid
         assert lib.pulse_adam_step_multi(plan._h, ctypes.byref(h), at + off, None) == invalid
     assert not raw.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_of_tiny_gradients(dtype):
+    """The small end of the norm's range: squares that are subnormal, and squares that are 0."""
+    _cuda()
+    n = 4096
+    for power, want in ((-63, 2.0 ** -57), (-70, 2.0 ** -64), (-74, 2.0 ** -68), (-76, 0.0), (-100, 0.0)):
+        norm, clip = _norm_plan([torch.full((n,), 2.0 ** power, dtype=dtype, device="cuda")]).grad_norm(1.0)
+        assert norm.item() == want and clip.item() == 1.0  # sums of equal powers of 2 are exact
+    g = (torch.rand(n + 5, device="cuda") * 1e-20).to(dtype)[5:]
+    want = np.sqrt(np.square(g.double().cpu().numpy()).sum())
+    # each of n squares is off by half of 2^-149, beside what larger gradients have
+    tol = 0.5 * n * 2.0 ** -150 / want ** 2 + NORM_TOL
+    assert abs(_norm_plan([g]).grad_norm(1.0)[0].item() - want) <= want * tol
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[33], [70001, 3, 8192], [5000011, 1 << 20]])
+def test_norm_sums_of_32(dtype, sizes):
+    """The documented accuracy: 32 squares in FP32, at most a rounding each, halved by the root, and two of the result."""
+    _cuda()
+    gen = torch.Generator(device="cuda").manual_seed(sizes[0])
+    grads = [torch.randn(n, generator=gen, device="cuda").to(dtype) for n in sizes]
+    want = np.sqrt(sum(float(np.square(g.double().cpu().numpy()).sum()) for g in grads))
+    assert abs(_norm_plan(grads).grad_norm(1.0)[0].item() - want) <= want * (32 / 2 + 2) * 2.0 ** -24
