@@ -744,7 +744,8 @@ int pulse_encode_noalloc(const float *master_f32, uint16_t *prev_bf16, uint64_t 
  *   d = lr * lr_scale * weight_decay
  * m and v are reproducible bit for bit (no fused multiply-add); the quotient
  * and the square root in w may be off by a few units in the last place of the
- * update, and a v below 2^-126 counts as 0 under the root. A grad_scale that is
+ * update. With 8-bit moments a v below 2^-126 counts as 0 under the root, which an eps
+ * below about 1e-17 would show. A grad_scale that is
  * not finite leaves w, m and v as they are (a step with non-finite gradients is
  * skipped without a host round trip).
  *

@@ -569,3 +569,23 @@ def test_norm_sums_of_32(dtype, sizes):
     grads = [torch.randn(n, generator=gen, device="cuda").to(dtype) for n in sizes]
     want = np.sqrt(sum(float(np.square(g.double().cpu().numpy()).sum()) for g in grads))
     assert abs(_norm_plan(grads).grad_norm(1.0)[0].item() - want) <= want * (32 / 2 + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_second_moments_below_the_normal_range(shift):
+    """FP32 moments: a subnormal v counts as it is under the root, beside an eps that is smaller still."""
+    _cuda()
+    n, eps = 3001, 2.0 ** -126
+    model = Model([n], 32, shift=shift, seed=23)
+    p = model.parts[0]
+    g = torch.randn(n, generator=torch.Generator().manual_seed(1)) * 2.0 ** -66
+    p["buf"]["g"].t.copy_(g)
+    for k in ("m", "v"):
+        p["buf"][k].t.zero_()
+    model.plan.step(1, LR, 0.0, 0.0, eps)
+    m, v = ref.moments32(g.numpy(), np.zeros(n), np.zeros(n), 0.0, 0.0)
+    assert (v < 2.0 ** -126).all() and (v > 0).sum() > n // 2
+    w, part = ref.weights64(p["w"], m, v, 1, LR, 0.0, 0.0, eps, float(np.float32(model.wd[0])), model.ls[0])
+    got = p["buf"]["w"].t.cpu().numpy()
+    assert np.all(np.abs(got - w) <= ref.weight_tolerance(w, part))
+    np.testing.assert_array_equal(p["buf"]["v"].t.cpu().numpy(), v)
