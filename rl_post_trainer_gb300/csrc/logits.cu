@@ -9,6 +9,13 @@
 // lists say, and nothing depends on the order of the tokens' atomics: bits are ORed
 // and counts are integers. Everything is computed in FP32, rounded step by step as the
 // formulas say, and rounded once more where the output is BF16.
+//
+// Quotients are products with the divisor's rounded reciprocal, one unit further from
+// the quotient than its own rounding at most. Dividing where a token was seen costs
+// instructions and registers (spills) in kernels that have neither to spare: 256 rows of
+// 128,256 with histories up to 8,192 take 66 us instead of 52.5, the gradient of 4,096
+// rows 545 instead of 453, 3,001 FP32 rows of 32,003 120 instead of 112.5; dividing by the
+// temperature too 76, 809 and 136.
 #include <type_traits>
 
 #include "pulse.h"
