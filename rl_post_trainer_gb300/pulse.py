@@ -1496,7 +1496,7 @@ class LogitsPlan:
             self.device = t.device
         elif t.device != self.device:
             raise ValueError(f"{name}: on {t.device}, expected {self.device}")
-        return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], self.vocab)
+        return t.data_ptr(), stride[0] if shape[0] > 1 else self.vocab  # a single row has no pitch, whatever its stride
 
     def shape(self, logits: torch.Tensor, out: Optional[torch.Tensor] = None,
               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
