@@ -930,6 +930,14 @@ int pulse_logits_shape_backward(const pulse_logits_shaping *shaping, uint64_t ro
                                 uint64_t dlogits_stride, cudaStream_t stream);
 
 /*
+ * pulse_logits_sorts -- sorts_out[0] (host) = 1 where such a call on the current
+ * device, forward or (backward != 0) backward, sorts its token list first, as described
+ * above, else 0. Results are the same either way.
+ */
+int pulse_logits_sorts(const pulse_logits_shaping *shaping, uint64_t rows, int backward,
+                       int *sorts_out);
+
+/*
  * Test hook for the look-back watchdog (not for production use). Runs
  * pulse_encode with a wait limit of `wait_limit_ns` nanoseconds while tile 0
  * is never processed, so tile 1 waits for a predecessor that never

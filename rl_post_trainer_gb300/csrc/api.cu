@@ -1832,14 +1832,23 @@ bool logits_reserve(LogitsWorkspace& w, uint64_t entries, uint64_t offs, cudaStr
   return true;
 }
 
+// Whether a call reads the histories: counts and presence have no part in the gradient.
+bool reads_history(const pulse_logits_shaping& s, bool backward) {
+  return s.tokens && (s.repetition || (!backward && (s.presence || s.frequency)));
+}
+
+// One CTA per slice of a row: rows fit the grid's second and third dimension.
+bool rows_fit(const pulse_logits_shaping& s, uint64_t rows) {
+  return rows <= (1ull << 30) && rows <= kMaxTiles / div_up(s.vocab, 1024);
+}
+
 // Fills the shaping's part and the stream's error word, and sorts the tokens
 // where `history` is read and the sorting pays. The caller holds g_ws_mu until it
 // has launched the kernel that takes *a. The handle of the per-thread default stream
 // names another stream in every thread, so calls on it share no sorted histories.
 int logits_args(const pulse_logits_shaping& s, uint64_t rows, bool history, cudaStream_t stream,
                 LogitsArgs* a) {
-  // one CTA per slice of a row: rows fit the grid's second and third dimension
-  if (rows > (1ull << 30) || rows > kMaxTiles / div_up(s.vocab, 1024)) return PULSE_ERR_RANGE;
+  if (!rows_fit(s, rows)) return PULSE_ERR_RANGE;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
   a->rows = rows;
@@ -1901,9 +1910,8 @@ int pulse_logits_shape(const pulse_logits_shaping* shaping, uint64_t rows, const
   if (!rows_ok(src, shaping->vocab) || !rows_ok(dst, shaping->vocab)) return PULSE_ERR_INVALID;
   if (!same_rows(src, dst) && rows_overlap(src, dst, rows, shaping->vocab)) return PULSE_ERR_INVALID;
   LogitsArgs a{};
-  const bool history = shaping->tokens && (shaping->repetition || shaping->presence || shaping->frequency);
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  const int st = logits_args(*shaping, rows, history, stream, &a);
+  const int st = logits_args(*shaping, rows, reads_history(*shaping, false), stream, &a);
   if (st != PULSE_OK) return st;
   a.src = logits;
   a.src_stride = stride;
@@ -1919,7 +1927,7 @@ int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t ro
   if (!shaping_ok(shaping) || !types_ok(in_type, out_type)) return PULSE_ERR_INVALID;
   if (rows == 0) return PULSE_OK;
   if (rows > kMaxTiles) return PULSE_ERR_RANGE;
-  const bool needs_raw = shaping->tokens && shaping->repetition;
+  const bool needs_raw = reads_history(*shaping, true);
   const RowsOf src{dout, dout_stride, out_type}, raw{logits, stride, in_type};
   const RowsOf dst{dlogits, dlogits_stride, in_type};
   if (!rows_ok(src, shaping->vocab) || !rows_ok(dst, shaping->vocab)) return PULSE_ERR_INVALID;
@@ -1937,6 +1945,23 @@ int pulse_logits_shape_backward(const pulse_logits_shaping* shaping, uint64_t ro
   a.dst = dlogits;
   a.dst_stride = dlogits_stride;
   return cuda_status(launch_logits_backward(a, in_type, out_type, stream));
+}
+
+int pulse_logits_sorts(const pulse_logits_shaping* shaping, uint64_t rows, int backward, int* sorts_out) {
+  if (!shaping_ok(shaping) || sorts_out == nullptr) return PULSE_ERR_INVALID;
+  *sorts_out = 0;
+  if (rows == 0 || !reads_history(*shaping, backward != 0)) return PULSE_OK;
+  if (!rows_fit(*shaping, rows)) return PULSE_ERR_RANGE;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
+  LogitsArgs a{};
+  a.rows = rows;
+  a.vocab = uint32_t(shaping->vocab);
+  a.ntokens = int64_t(shaping->ntokens);
+  const int sms = sm_count(device);
+  logits_cut(a, sms);
+  *sorts_out = logits_sorts(a, sms) ? 1 : 0;
+  return PULSE_OK;
 }
 
 }  // extern "C"

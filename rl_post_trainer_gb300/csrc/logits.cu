@@ -751,10 +751,11 @@ void logits_cut(LogitsArgs& a, int sms) {
 // waves of slices. What the rows read of the token list is known on the device only;
 // two bounds stand for it: the list read once by each slice, and, for a list that rows
 // share, up to a token more with each row. Times unsorted and sorted, in us, of BF16
-// rows of 128,256 with a quarter to all of the given history: 64 rows of 32,768 33, 37;
-// 128 of 8,192 26, 29; 128 of 32,768 53, 48; 256 of 2,048 37, 38; 256 of 8,192 49, 45;
-// 256 of 32,768 98, 78; 1,024 of 8,192 169, 152. Rows of one sequence: gradients of
-// 1,024 108, 111, of 2,048 217, 219, of 4,096 470, 457. The list should also be small
+// rows of 128,256 with a quarter to all of the given history: 64 rows of 32,768 31, 36;
+// 128 of 8,192 24, 27; 128 of 32,768 52, 48; 256 of 2,048 34, 35; 256 of 8,192 46, 45;
+// 256 of 32,768 94, 78; 512 of 2,048 62, 63; 512 of 8,192 86, 81; 1,024 of 8,192 164, 153.
+// Rows of one sequence: gradients of 1,024 104, 109, of 2,048 213, 215, of 4,096 467,
+// 453. The list should also be small
 // next to the rows, as it is all sorted, used or not.
 bool logits_sorts(const LogitsArgs& a, int sms) {
   const uint64_t n = uint64_t(a.ntokens), ctas = a.rows * a.slices;

@@ -274,6 +274,7 @@ def lib():
             "pulse_logits_shape": ([ctypes.POINTER(PulseLogitsShaping), U64, P, U64, I, P, U64, I, P], I),
             "pulse_logits_shape_backward": ([ctypes.POINTER(PulseLogitsShaping), U64, P, U64, I,
                                              P, U64, I, P, U64, P], I),
+            "pulse_logits_sorts": ([ctypes.POINTER(PulseLogitsShaping), U64, I, ctypes.POINTER(I)], I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -1478,6 +1479,15 @@ class LogitsPlan:
             p["bias_tokens"], p["bias_values"], nbias, p["bias_begin"], p["mask"], mask_rows,
             mask_stride, p["mask_row"])
         self._ref = ctypes.byref(self._c)
+
+    def sorts(self, rows: Optional[int] = None, backward: bool = False) -> bool:
+        """Whether a call of that many rows (by default all) sorts its token list
+        first, which long histories of many rows are worth; the results are the same."""
+        out = ctypes.c_int()
+        with torch.cuda.device(self.device):
+            st = lib().pulse_logits_sorts(self._ref, self.rows if rows is None else rows, int(backward), ctypes.byref(out))
+        _raise(st, "pulse_logits_sorts")
+        return out.value != 0
 
     def _rows_of(self, t: torch.Tensor, name: str, dtypes, like: Optional[torch.Tensor] = None):
         """(pointer, pitch in elements) of rows of logits or their gradient."""

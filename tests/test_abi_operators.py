@@ -150,3 +150,16 @@ def test_misaligned_settings_are_refused(lib):
         assert lib.pulse_logits_shape_backward(s, 4, P(B), 100, 0, P(2 * C), 100, 0, P(C), 100, P(0)) == E.PULSE_ERR_INVALID
         assert lib.pulse_logits_shape(s, 0, P(B), 100, 0, P(C), 100, 0, P(0)) == E.PULSE_ERR_INVALID, name
     assert lib.pulse_logits_shape(shaping(**full), 0, P(B), 100, 0, P(C), 100, 0, P(0)) == E.PULSE_OK
+
+
+def test_sorts_arguments(lib):
+    out = ctypes.c_int(7)
+    assert lib.pulse_logits_sorts(None, 4, 0, ctypes.byref(out)) == E.PULSE_ERR_INVALID
+    assert lib.pulse_logits_sorts(shaping(vocab=0), 4, 0, ctypes.byref(out)) == E.PULSE_ERR_INVALID
+    assert lib.pulse_logits_sorts(shaping(), 4, 0, None) == E.PULSE_ERR_INVALID
+    hist = dict(tokens=A, begin=A, end=A, ntokens=1 << 30)
+    for s, rows, backward in ((shaping(), 4, 0), (shaping(**hist), 4, 0), (shaping(**hist, frequency=A), 4, 1),
+                              (shaping(**hist, repetition=A), 0, 0)):
+        out.value = 7
+        assert lib.pulse_logits_sorts(s, rows, backward, ctypes.byref(out)) == E.PULSE_OK and out.value == 0
+    assert lib.pulse_logits_sorts(shaping(**hist, repetition=A), 1 << 40, 0, ctypes.byref(out)) == E.PULSE_ERR_RANGE
