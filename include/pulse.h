@@ -839,7 +839,12 @@ int pulse_grad_norm_multi(pulse_adam_plan *plan, float max_norm, float *norm_out
 
 /* One AdamW step over every tensor that has a gradient. grad_scale: device,
  * one float, or NULL. Errors: PULSE_ERR_INVALID (also a plan in which a tensor
- * with n > 0 lacks master, m or v, or the exponent bytes of 8-bit moments). */
+ * with n > 0 lacks master, m or v, or the exponent bytes of 8-bit moments).
+ * Captured into a graph, the step keeps everything in *hyper: each replay has the bias
+ * correction of that step number, that rate, and the random bits of that seed and step
+ * for the rounding of 8-bit moments. What it reads on the device (grad_scale, gradients
+ * and the pointers to them, weights, moments) is read at each replay. A training loop
+ * captures a step anew, or launches it outside the graph, for every step number. */
 int pulse_adam_step_multi(pulse_adam_plan *plan, const pulse_adam_hyper *hyper,
                           const float *grad_scale, cudaStream_t stream);
 

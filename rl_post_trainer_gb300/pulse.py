@@ -1355,7 +1355,8 @@ class AdamPlan:
              grad_scale: Optional[torch.Tensor] = None, seed: int = 0):
         """One AdamW step in place (``step`` is 1 for the first). ``grad_scale``:
         one FP32 value on the device that multiplies the gradients; ``seed``: of
-        the stochastic rounding of 8-bit moments."""
+        the stochastic rounding of 8-bit moments. A step captured into a CUDA graph keeps
+        its number, rates and random bits in every replay."""
         if step < 1:
             raise ValueError(f"step: {step}, the first step is 1")
         scale = 0
