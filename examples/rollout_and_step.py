@@ -14,7 +14,9 @@ rewarded for tokens of one kind, and learns:
 4. Plan.encode: the BF16 patch of what the step moved -> Plan.apply on the sampler
 
 At the end of every iteration the sampler's weights equal the trainer's BF16 view
-bit for bit, and the log-probabilities that the sampler saw equal the trainer's.
+bit for bit. Logits of the same bits are shaped to the same bits by the sampler's plan
+and the trainer's; the log-probabilities that the two see differ only where a last bit
+of a BF16 logit does, their matrix products being of different heights.
 """
 from __future__ import annotations
 
@@ -67,15 +69,10 @@ def logits_of(weights, tokens: torch.Tensor) -> torch.Tensor:
     return weights[0][tokens.long()] @ weights[1].t()
 
 
-def run(iterations: int = 30, state_bits: int = 8, seed: int = 0, lr: float = 0.1):
-    """Mean reward of every iteration, and the largest difference of log-probabilities."""
-    dev = torch.device("cuda", 0)
-    gen = torch.Generator(device=dev).manual_seed(seed)
-    trainer = Trainer(state_bits, gen)
-    sampler = Sampler(trainer)
-
-    total = PROMPT + LENGTH
-    tokens = torch.zeros(SEQUENCES, total, dtype=torch.int32, device=dev)
+def plans(tokens: torch.Tensor):
+    """The sampler's plan (a row a sequence, its history up to `end`) and the trainer's (a row a
+    generated position, in the order of the sequences), with the same settings; `split`, `end`."""
+    dev, total = tokens.device, tokens.shape[1]
     begin = torch.arange(SEQUENCES, device=dev) * total
     split, end = begin + PROMPT, begin + PROMPT
     settings = {"repetition": 1.05, "presence": 0.1, "frequency": 0.05, "temperature": 0.9}
@@ -96,7 +93,18 @@ def run(iterations: int = 30, state_bits: int = 8, seed: int = 0, lr: float = 0.
     decode = plan(1, begin, split, end)
     step = torch.arange(LENGTH, device=dev).repeat(SEQUENCES)
     wide = [t.repeat_interleave(LENGTH) for t in (begin, split)]
-    train = plan(LENGTH, wide[0], wide[1], wide[1] + step)
+    return decode, plan(LENGTH, wide[0], wide[1], wide[1] + step), split, end
+
+
+def run(iterations: int = 30, state_bits: int = 8, seed: int = 0, lr: float = 0.1):
+    """Mean reward of every iteration, and the largest difference of log-probabilities."""
+    dev = torch.device("cuda", 0)
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    trainer = Trainer(state_bits, gen)
+    sampler = Sampler(trainer)
+
+    tokens = torch.zeros(SEQUENCES, PROMPT + LENGTH, dtype=torch.int32, device=dev)
+    decode, train, split, end = plans(tokens)
 
     rewards, apart = [], 0.0
     for iteration in range(1, iterations + 1):
