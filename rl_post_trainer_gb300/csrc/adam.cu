@@ -103,12 +103,15 @@ __device__ __forceinline__ F8 ld_grad8(const AdamTensorDesc& d, uint64_t i) {
 }
 
 // Each element is read and written once, 26 bytes of traffic with BF16 gradients and
-// 28 with FP32 ones, for 26 instructions: bound by memory (it issues in 18 % of its
+// 28 with FP32 ones, for 36 instructions: bound by memory (it issues in 25 % of its
 // cycles). A thread takes one group of 8, whose four loads are all on their way
 // before the first is used, and a tile is a CTA's 2,048 elements, so nothing loops.
 // 1.54 billion parameters in a decoder's tensors with BF16 gradients: 5.60 ms, 7.17
 // TB/s, where a plain copy moves 6.76 TB/s; two groups a thread 6.61 ms, tiles of
-// 4,096 to 16,384 5.66 to 5.81 ms, 3 or 5 CTAs per SM 5.73 ms.
+// 4,096 to 16,384 5.66 to 5.81 ms, 3 or 5 CTAs per SM 5.73 ms. Tensors whose buffers have no
+// common offset go an element a thread, whose narrow accesses cost them half of that
+// rate: 60 million parameters with BF16 gradients one element off take 447 us, 221 with all
+// on their groups or all one element off.
 constexpr int kAdam32Ctas = 4;  // CTAs per SM: 64 registers a thread
 __global__ void __launch_bounds__(kAdamThreads, kAdam32Ctas)
     adam32_kernel(const __grid_constant__ AdamLaunch a) {
@@ -480,8 +483,10 @@ __device__ __forceinline__ void adam8_blocks(const AdamLaunch& a, const Adam8Ptr
 // MIXED: some tensor of the plan is not aligned for groups throughout. The kernel
 // for aligned plans keeps its registers without the code for the others (3.41 ms
 // against 3.48 with both in one). The other way of the general one serves whole
-// blocks at any offset of weights and gradients: 60 million parameters shifted by one
-// element take 169 us (503 when each lane's elements were 32 apart).
+// blocks at any offset of weights and gradients: 60 million parameters with weights, BF16
+// gradients or both one element off take 164 to 166 us (503 when each lane's elements were
+// 32 apart), 136 on their groups; with FP32 gradients 188 and 143. Its element by element
+// accesses are what that costs, and a few registers too many (112 bytes of them reread).
 template <bool MIXED>
 __global__ void __launch_bounds__(kAdamThreads, kAdam8Ctas) adam8_kernel(const __grid_constant__ AdamLaunch a) {
   stream_ready();

@@ -26,7 +26,9 @@ namespace pulse {
 namespace {
 
 constexpr int kThreads = 256;
-// CTAs per SM: as many as the registers of a slice's groups leave (one more spills).
+// CTAs per SM: as many as the registers of a slice's groups leave. One more spills; the
+// FP32 gradient, which holds the raw logits beside its groups, spills as it is (168 bytes
+// stored and 196 loaded a thread: 2,000 rows of 32,003 take 99 us for 76 us of bytes).
 template <typename TSrc>
 constexpr int kMinCtas = sizeof(TSrc) == 4 ? 4 : 5;
 // Groups of 8 elements a thread holds: its whole part of a slice, asked for before the
@@ -105,7 +107,7 @@ __device__ __forceinline__ uint32_t lead_of(const T* p) {
 // A row's settings. Ranges that do not fit their lists
 // are empty (and recorded).
 struct RowSettings {
-  const int32_t* tokens;   // the history; null where the tokens are sorted
+  const int32_t* tokens;   // the history; not read where the tokens are sorted
   uint32_t history, made;  // its length, and where its generated part starts
   uint32_t block, from;    // sorted tokens: first block, and the history's place in it
   uint32_t biased;         // length of the bias list
@@ -510,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) scale_kernel(const __
 //   y = (p(x) - f * n - (n > 0 ? presence : 0) + b) * (1/T), p(x) as above, n the times
 //   that the token was generated, -inf where the mask is closed
 // A word a place is zeroed for all logits and read for groups of 8 with a token that a
-// list names (1,024 rows with up to 64 tokens each: 93 us, 8 more when all were read).
+// list names (1,024 rows with up to 64 tokens each: 95 us, 8 more when all were read).
 // Zeroing the named ones alone took a second pass over the history and a third barrier,
 // and was slower everywhere. Instructions and the waits between the barriers bound this
 // kernel (issue slots 47 %, DRAM 21 %): 256 BF16 rows of 128,256 with histories up to
-// 8,192, 100 biases and half of the rows masked take 51 us, 27 us with up to 64 tokens
+// 8,192, 100 biases and half of the rows masked take 52 us, 27 us with up to 64 tokens
 // and neither biases nor masks, where the logits alone would move in 20.
 template <typename TIn, typename TOut>
 __global__ void __launch_bounds__(kThreads, kMinCtas<TIn>) shape_kernel(const __grid_constant__ LogitsArgs a) {

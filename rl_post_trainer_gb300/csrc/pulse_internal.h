@@ -404,7 +404,7 @@ struct AdamLaunch {
   float beta2, one_minus_beta2;
   float inv_sqrt_bc2;             // 1 / sqrt(1 - beta2^step)
   float eps;
-  float one;                      // 1.0f (see add2 in adam.cu)
+  float one;                      // 1.0f (see the sums in adam8_block_full)
   uint32_t key;                   // seed and step folded
 };
 
