@@ -64,3 +64,30 @@ def test_threads_on_one_stream(stream):
     assert not failed, failed
     assert not wrong
     assert pulse.get_error(torch.device("cuda", 0)) == 0
+
+
+def test_threads_on_their_default_streams():
+    """cudaStreamPerThread: one handle, a stream of its own in every thread."""
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    rows, per_thread = 12, 2
+    plans = [_plan(rows, 12000 * k, k) for k in (1, 2, 3)]
+    x = torch.randn(rows, VOCAB, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    want = [p.shape(x) for p in plans]
+    outs = [[torch.zeros_like(x) for _ in range(10)] for _ in plans]
+    torch.cuda.synchronize()
+    status = []
+
+    def work(p, many):
+        torch.cuda.set_device(0)
+        for out in many:
+            status.append(pulse.lib().pulse_logits_shape(p._ref, rows, x.data_ptr(), VOCAB, 0, out.data_ptr(), VOCAB, 0, per_thread))
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(plans, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [0] * 30
+    assert all(torch.equal(out, y) for many, y in zip(outs, want) for out in many)
