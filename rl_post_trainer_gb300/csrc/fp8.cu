@@ -7,14 +7,16 @@
 // q + (x - q * scale) * r in fused operations (Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990). A quotient that is off by its
 // last bit would land on the other side of a tie between two codes, and in BF16 inputs
-// ties are frequent: their values are short fractions of the block's largest.
+// ties are frequent: their values are short fractions of the block's largest. The correction needs x - q * scale exactly.
+// That is a multiple of 2^-57 of the scale's binade (x above 2^-11 of it: smaller ones have code 0 whatever their last
+// bits), so below a scale of 2^-92 it could pass the smallest FP32 number: blocks below 2^-90 are lifted by 2^64 first.
 // amax takes a NaN along, and across lanes it is a maximum of bit patterns without the sign, under which NaN lies above
 // infinity, infinity above every number: a block with either of them is found by the same maximum.
 //
 // Every kernel is bound by memory: an element is read once, its code written once, and
 // everything between stays in registers. Measured, of the 6.8 TB/s of a copy: the view of 151936 x 1536 BF16 weights
-// (701 MB) 101 us, 6.9 TB/s; 16384 x 4096 BF16 activations through the norm with a residual (472 MB) 75 us, 6.2 TB/s;
-// rows off 16 bytes, 20011 x 5003 BF16, 77 us, 3.9 TB/s, bound by instructions: accesses of 2 and 1 bytes.
+// (701 MB) 102 us, 6.9 TB/s; 16384 x 4096 BF16 activations through the norm with a residual (472 MB) 75 us, 6.2 TB/s;
+// rows off 16 bytes, 20011 x 5003 BF16, 79 us, 3.8 TB/s, bound by instructions: accesses of 2 and 1 bytes.
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -27,6 +29,7 @@ namespace pulse {
 namespace {
 
 constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126
+constexpr float kSmallScale = 0x1p-90f, kLift = 0x1p64f;
 
 // ------------------------------------------------------------------ layouts
 //
@@ -200,7 +203,7 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
 __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-// Codes of x[0] .. x[3], whose negatives `n` holds: (q s - x)(-1 / s) + q, two at a time. With these signs -0 stays -0.
+// Codes of x[0] .. x[3], whose negatives `n` holds, with divisor s: (q s - x)(-1 / s) + q, two at a time. With these signs -0 stays -0.
 __device__ __forceinline__ uint32_t codes4(const float* n, float s, float inv) {
   const unsigned long long s2 = pair_of(s, s), i2 = pair_of(-inv, -inv);
   uint32_t c[2];
@@ -215,6 +218,15 @@ __device__ __forceinline__ uint32_t codes4(const float* n, float s, float inv) {
     c[k] = codes2(lo, hi);
   }
   return __byte_perm(c[0], c[1], 0x5410);
+}
+
+// The divisor of kCount values, whose negatives are `n`: their scale, both lifted where it is small.
+template <int kCount>
+__device__ __forceinline__ float divisor_of(float* n, float s) {
+  if (!(s < kSmallScale)) return s;
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) n[k] = __fmul_rn(n[k], kLift);
+  return __fmul_rn(s, kLift);
 }
 
 // Scales of the runs: packed, s[0] is the own run's.
@@ -235,16 +247,16 @@ __device__ __forceinline__ void scales_of(const float (&x)[kEach<T>], float (&s)
   }
 }
 
-// Codes of the warp's runs, whose negatives are `n`: `at(h)` gives run h's.
-template <typename T, bool kLoose, bool kFull, typename At>
-__device__ __forceinline__ void store_codes(At at, const float (&n)[kEach<T>], const float (&s)[kRuns<T>]) {
+// Codes of the warp's runs, whose negatives are `n` (not needed after): `at(h)` gives run h's. kUsual: no scale is small.
+template <typename T, bool kLoose, bool kFull, bool kUsual = false, typename At>
+__device__ __forceinline__ void store_codes(At at, float (&n)[kEach<T>], const float (&s)[kRuns<T>]) {
   if constexpr (!kLoose) {
     const Run<uint8_t> r = at(own_run<T>());
     const uint32_t col = own_col<T>();
-    const float inv = __frcp_rn(s[0]);
+    const float d = kUsual ? s[0] : divisor_of<kEach<T>>(n, s[0]), inv = __frcp_rn(d);
     uint32_t c[kEach<T> / 4];
 #pragma unroll
-    for (int k = 0; k < kEach<T> / 4; ++k) c[k] = codes4(n + 4 * k, s[0], inv);
+    for (int k = 0; k < kEach<T> / 4; ++k) c[k] = codes4(n + 4 * k, d, inv);
     uint8_t* p = r.p + col;
     if (col + kEach<T> <= r.left) {
       if constexpr (kEach<T> == 8)
@@ -257,11 +269,16 @@ __device__ __forceinline__ void store_codes(At at, const float (&n)[kEach<T>], c
         if (col + k < r.left) p[k] = uint8_t(c[k >> 2] >> (8 * (k & 3)));
     }
   } else {
+    float d[kRuns<T>], least = s[0];
+#pragma unroll
+    for (int h = 0; h < kRuns<T>; ++h) d[h] = s[h], least = fminf(least, s[h]);
+    if (!kUsual && least < kSmallScale)  // one branch for all runs
+#pragma unroll
+      for (int h = 0; h < kRuns<T>; ++h) d[h] = divisor_of<4>(n + h * 4, s[h]);
 #pragma unroll
     for (int h = 0; h < kRuns<T>; ++h) {
       const Run<uint8_t> r = at(h);
-      const float inv = __frcp_rn(s[h]);
-      const uint32_t c = codes4(n + h * 4, s[h], inv);
+      const uint32_t c = codes4(n + h * 4, d[h], __frcp_rn(d[h]));
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j)
         if (kFull || loose_col(j) < r.left) r.p[loose_col(j)] = uint8_t(c >> (8 * j));
@@ -390,12 +407,12 @@ __global__ void __launch_bounds__(kTallThreads, sizeof(T) == 4 ? 2 : kLoose ? 3 
 #pragma unroll
   for (int h = 0; h < kRuns<T>; ++h) s[h] = scale_of(m);
   if (threadIdx.x == 0) a.scales[uint64_t(group) * a.scales_stride + block] = s[0];
-  auto store = [&](auto all) {
+  auto store = [&](auto all, auto usual) {
 #pragma unroll
     for (int j = 0; j < kTallTurns<T>; ++j) {
       float x[kEach<T>];  // the negatives
       unpack(negated(raw[j], static_cast<const T*>(nullptr)), x);
-      store_codes<T, kLoose, decltype(all)::value>(
+      store_codes<T, kLoose, decltype(all)::value, decltype(usual)::value>(
           [&](uint32_t h) {
             const uint64_t row = row_of(j, h);
             const bool in = decltype(all)::value || row < a.rows;
@@ -404,10 +421,13 @@ __global__ void __launch_bounds__(kTallThreads, sizeof(T) == 4 ? 2 : kLoose ? 3 
           x, s);
     }
   };
-  if (full)
-    store(std::true_type{});
+  // one choice for all: with one in each set 151936 x 1536 took 104 us instead of 102
+  if (s[0] < kSmallScale)
+    store(std::false_type{}, std::false_type{});
+  else if (full)
+    store(std::true_type{}, std::true_type{});
   else
-    store(std::false_type{});
+    store(std::false_type{}, std::true_type{});
 }
 
 // --------------------------------------------------------------- RMS norm
