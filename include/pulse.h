@@ -979,10 +979,9 @@ int pulse_fp8_quantize(const void *x, uint64_t rows, uint64_t cols, uint64_t str
  * (block_rows 1) of the result:
  *   h = x + residual, rounded to `type` and stored in sum_out  (residual NULL: h = x)
  *   y = h / sqrt(mean of h^2 over the row + eps) * weight      (weight NULL: 1)
- * in FP32; y is quantised without a rounding in between. A row that holds a NaN
- * or an infinity, or whose sum of squares passes FP32's range (|h| above about
- * 1e18), has no norm: an infinity or NaN in h gives NaN scales and codes 0x7F in
- * its block at least, a sum past the range zeros.
+ * in FP32; y is quantised without a rounding in between. Rows whose squares pass
+ * FP32's range at either end are scaled by a power of two first. A row that holds
+ * a NaN or an infinity has no norm: NaN scales and codes 0x7F in that block at least.
  *   x, residual, sum_out  of `type` (PULSE_F32 or PULSE_BF16); sum_out goes with
  *                         residual, and may be x or residual itself (same stride)
  *   weight                cols values of weight_type

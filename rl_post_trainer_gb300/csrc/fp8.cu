@@ -487,6 +487,88 @@ __device__ __forceinline__ void load_weight(const Fp8Args& a, uint32_t col, floa
   }
 }
 
+// Two sums of squares in one register pair.
+template <int kCount>
+__device__ __forceinline__ void add_squares(unsigned long long& squares, const float (&v)[kCount]) {
+#pragma unroll
+  for (int k = 0; k < kCount; k += 2) {
+    const unsigned long long p = pair_of(v[k], v[k + 1]);
+    fma2(squares, p, p);
+  }
+}
+// Of all threads; `part`: one for each warp, with a barrier before it is used again.
+__device__ __forceinline__ float sum_of(float v, float* part) {
+  const uint32_t warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+__device__ __forceinline__ float mean_of(const Fp8Args& a, unsigned long long squares, float* part) {
+  float lo, hi;
+  unpair(squares, lo, hi);
+  return __fadd_rn(__fdiv_rn(sum_of(lo + hi, part), float(a.cols)), a.eps);
+}
+// Squares are off by 2^-150 each, no more than 2^-50 of a mean (with eps) in this range. NaN, too, has no better one.
+__device__ __forceinline__ bool fits(float mean) { return !(mean < 0x1p-100f || mean > 3.4028234e38f); }
+
+// The CTA's rows whose mean does not fit, once more: read again, times a power of two that takes a row's largest, or the
+// root of eps, near 1. All rows' sums are taken again, in the same order, to know which they are: noted down, or treated in the
+// loop itself, they cost the other rows (16384 x 4096 BF16 without residual 53 to 55 us instead of 50).
+template <typename T, bool kLoose>
+__device__ __noinline__ void norm_lifted(const Fp8Args& args, float (&part)[2][32]) {
+  const Fp8Args a = args;
+  constexpr uint32_t kWide = kRuns<T> * 128;
+  const uint32_t warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const NormRow<T, kLoose> now{a, row};
+    auto each = [&](auto f) {  // a thread reads what it has stored of the sum itself
+#pragma unroll 1
+      for (uint32_t col = warp * kWide; col < a.cols; col += warps * kWide) {
+        float v[kEach<T>];
+        unpack(a.residual ? now.load(a.sum, a.sum_stride, col) : now.load(a.x, a.stride, col), v);
+        f(col, v);
+      }
+    };
+    unsigned long long squares = 0;
+    each([&](uint32_t, float (&v)[kEach<T>]) { add_squares<kEach<T>>(squares, v); });
+    __syncthreads();
+    if (fits(mean_of(a, squares, part[0]))) continue;
+    uint32_t most = 0;
+    each([&](uint32_t, float (&v)[kEach<T>]) {
+#pragma unroll
+      for (int k = 0; k < kEach<T>; ++k) most = max(most, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+    });
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) part[1][warp] = __uint_as_float(most);
+    __syncthreads();
+    most = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? __float_as_uint(part[1][lane]) : 0u);
+    int up = 127 - int(most >> 23);
+    if (a.eps > 0.0f) up = min(up, (127 - int(__float_as_uint(a.eps) >> 23)) / 2);
+    const float lift = __uint_as_float(uint32_t(max(-126, min(126, up)) + 127) << 23);
+    float ss = 0.0f;
+    each([&](uint32_t, float (&v)[kEach<T>]) {
+#pragma unroll
+      for (int k = 0; k < kEach<T>; ++k) {
+        v[k] = __fmul_rn(v[k], lift);
+        ss = __fmaf_rn(v[k], v[k], ss);
+      }
+    });
+    const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum_of(ss, part[0]), float(a.cols)), __fmul_rn(__fmul_rn(a.eps, lift), lift)));
+    each([&](uint32_t col, float (&v)[kEach<T>]) {
+      float g[kEach<T>];
+      load_weight<T, kLoose>(a, col, g);
+#pragma unroll
+      for (int k = 0; k < kEach<T>; ++k) v[k] = __fmul_rn(v[k], lift);
+      now.store(col, v, g, rstd);
+    });
+  }
+}
+
 template <typename T>
 constexpr int kNormThreads = 8192 / kEach<T>;  // a row of 8192 columns
 
@@ -514,22 +596,16 @@ __global__ void __launch_bounds__(kNormThreads<T>, sizeof(T) == 2 && kTurns < 2 
     for (int t = 0; t < kKeep; ++t) load_weight<T, kLoose>(a, col_of(t), g[t]);
   }
   int turn = 0;
+  bool whole = true;  // FP32 has held every mean square so far
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const NormRow<T, kLoose> now{a, row};
     float h[kKeep][kEach<T>];
-    unsigned long long squares = 0;  // two sums
-    auto square = [&](const float (&v)[kEach<T>]) {
-#pragma unroll
-      for (int k = 0; k < kEach<T>; k += 2) {
-        const unsigned long long p = pair_of(v[k], v[k + 1]);
-        fma2(squares, p, p);
-      }
-    };
+    unsigned long long squares = 0;
     if (kTurns) {
 #pragma unroll
       for (int t = 0; t < kKeep; ++t) {
         now.add(col_of(t), x[t], res[t], h[t]);
-        square(h[t]);
+        add_squares<kEach<T>>(squares, h[t]);
       }
       if (row + gridDim.x < a.rows) ask(row + gridDim.x);
     } else {
@@ -537,21 +613,12 @@ __global__ void __launch_bounds__(kNormThreads<T>, sizeof(T) == 2 && kTurns < 2 
         x[0] = now.load(a.x, a.stride, col);
         if (a.residual) res[0] = now.load(a.residual, a.residual_stride, col);
         now.add(col, x[0], res[0], h[0]);
-        square(h[0]);
+        add_squares<kEach<T>>(squares, h[0]);
       }
     }
-    float ss, other;
-    unpair(squares, ss, other);
-    ss += other;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
     // two sets of parts: a warp may be a row ahead of one that still reads
-    if (lane == 0) part[turn][warp] = ss;
-    __syncthreads();
-    ss = lane < warps ? part[turn][lane] : 0.0f;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-    const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, float(a.cols)), a.eps));
+    const float mean = mean_of(a, squares, part[turn]), rstd = __frsqrt_rn(mean);
+    whole = whole && fits(mean);
     if (kTurns) {
 #pragma unroll
       for (int t = 0; t < kKeep; ++t) now.store(col_of(t), h[t], g[t], rstd);
@@ -563,6 +630,7 @@ __global__ void __launch_bounds__(kNormThreads<T>, sizeof(T) == 2 && kTurns < 2 
       }
     }
   }
+  if (!whole) norm_lifted<T, kLoose>(a, part);
 }
 
 template <typename T, bool kLoose>
