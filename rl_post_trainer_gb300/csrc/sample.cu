@@ -35,6 +35,7 @@
 #include "pulse.h"
 #include "pulse_device.cuh"
 #include "pulse_internal.h"
+#include "slice_edges.h"
 
 namespace pulse {
 namespace {
@@ -483,8 +484,8 @@ struct Slice {
   uint32_t pieces;
   const uint4* kept;  // kResident: the pieces in shared memory
 
-  // From global memory. A piece that is cut off is read whole, too, and what is not of the slice replaced: it belongs to
-  // the matrix's own range of addresses, but for the first piece of its first row and the last of its last. Those are read
+  // From global memory. A piece that is cut off is read whole, too, and what is not of the slice replaced, but for pieces that
+  // leave the matrix's own range of addresses (slice_edges). Those are read
   // by elements, in a function of its own (inlined, it would be most of the kernel's code).
   bool low_edge, high_edge;
   __device__ bool at_edge(uint32_t i) const { return (i == 0 && low_edge) || (i + 1 == pieces && high_edge); }
@@ -675,10 +676,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, uint3
   slice.count = min(a.vocab - slice.begin, per);
   slice.row = static_cast<const T*>(a.logits) + row * a.stride + slice.begin;
   slice.lead = uint32_t(reinterpret_cast<uintptr_t>(slice.row) & 15u) / sizeof(T);
-  slice.pieces = (slice.lead + slice.count + kPiece - 1) / kPiece;
+  const SliceEdges edges = slice_edges(row * a.stride + slice.begin, slice.count, slice.lead, kPiece, (a.rows - 1) * a.stride + a.vocab);
+  slice.pieces = edges.pieces;
   slice.kept = pieces;
-  slice.low_edge = row == 0 && slice.begin == 0 && slice.lead != 0;
-  slice.high_edge = row + 1 == a.rows && slice.begin + slice.count == a.vocab;
+  slice.low_edge = edges.low;
+  slice.high_edge = edges.high;
 
   Settings s;
   s.t = a.temperature ? a.temperature[row] : 1.0f;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, uint3
     if (kResident) pieces[i] = q;
     most = max_with(q, most, static_cast<const T*>(nullptr));
   };
-  const uint32_t p0 = slice.low_edge ? 1 : 0, p1 = slice.pieces - (slice.high_edge && slice.pieces ? 1 : 0);
+  const uint32_t p0 = slice.low_edge ? 1 : 0, p1 = slice.pieces - (slice.high_edge ? 1 : 0);
   constexpr int kAhead = 8;
   for (uint32_t i = p0 + threadIdx.x; i < p1; i += kThreads * kAhead) {
     uint4 q[kAhead];
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, uint3
     for (int j = 0; j < kAhead; ++j)
       if (i + j * kThreads < p1) take(i + j * kThreads, slice.partial(i + j * kThreads) ? slice.masked(i + j * kThreads, q[j]) : q[j]);
   }
-  if (threadIdx.x == 0 && p0 && slice.pieces) take(0, slice.edge(0));
+  if (threadIdx.x == 0 && p0) take(0, slice.edge(0));
   if (threadIdx.x == 32 && p1 < slice.pieces && p1 >= p0) take(p1, slice.edge(p1));
 
   if (threadIdx.x < 64) sh.table[threadIdx.x] = entry;
