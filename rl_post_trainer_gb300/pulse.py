@@ -17,6 +17,7 @@ import os
 from typing import Optional, Sequence
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import _build
 
@@ -1250,7 +1251,7 @@ def _call(name: str, dev: torch.device, *args):
 
 
 def _overwritten(t: torch.Tensor):
-    """Tells autograd that an input's values are gone: a backward pass that saved them has to fail."""
+    """Tells autograd that a given tensor's values are gone: a backward pass that saved them has to fail."""
     if not t.is_inference():
         torch.autograd.graph.increment_version(t)
 
@@ -1573,6 +1574,9 @@ class LogitsPlan:
 
 
 # ------------------------------------------------------------- FP8 serving path
+#
+# Serving operators: they give no gradients. Arguments that require one or carry a tangent are refused (sampling takes
+# such logits); buffers that the caller gives count as overwritten in place, as autograd sees them.
 
 FP8_BLOCK = 128
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
@@ -1590,18 +1594,29 @@ def _rows_error(t, name: str, dtypes, dev, rows, cols):
         return ValueError(f"{name}: rows must be contiguous")
     if dev is not None and t.device != dev:
         return ValueError(f"{name}: on {t.device}, expected {dev}")
-    return ValueError(f"{name}: requires a gradient, which this operator does not have (detach it, or call under no_grad)")
+    return _wanted_error(t, name)
+
+
+def _wants_more(t: torch.Tensor) -> bool:
+    """Whether autograd is asked for what these operators do not give: a gradient, or a tangent that ``t`` carries."""
+    return (t.requires_grad and torch.is_grad_enabled()) or (
+        _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None)
+
+
+def _wanted_error(t: torch.Tensor, name: str) -> ValueError:
+    what = "requires a gradient" if t.requires_grad and torch.is_grad_enabled() else "carries a tangent"
+    return ValueError(f"{name}: {what}, which this operator does not have (detach it, or call under no_grad)")
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, dev=None, rows=None, cols=None, grad=False):
     """(pointer, rows, columns, stride in elements) of a matrix with contiguous rows. Tensors that require a
-    gradient are refused: these operators give none (``grad``: this argument's is not asked for). Small calls
-    take as long as their checks, so everything is read once."""
+    gradient or carry a tangent are refused: these operators give none (``grad``: this argument's is not asked
+    for). Small calls take as long as their checks, so everything is read once."""
     try:
         m, n = t.shape
         step, one = t.stride()
         ok = (t.dtype in dtypes and t.is_cuda and (one == 1 or n <= 1) and (rows is None or (m == rows and n == cols))
-              and (dev is None or t.device == dev) and not (t.requires_grad and not grad and torch.is_grad_enabled()))
+              and (dev is None or t.device == dev) and (grad or not (t.requires_grad or _forward._current_level >= 0) or not _wants_more(t)))
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
@@ -1609,10 +1624,12 @@ def _rows(t: torch.Tensor, name: str, dtypes, dev=None, rows=None, cols=None, gr
     return t.data_ptr(), m, n, step if m > 1 else n  # a single row has no pitch, whatever its stride
 
 
-def _vector(t: torch.Tensor, name: str, dtype, dev, n: int) -> int:
-    """The pointer of a contiguous vector of ``n``."""
+def _vector(t: torch.Tensor, name: str, dtype, dev, n: int, grad=False) -> int:
+    """The pointer of a contiguous vector of ``n``; ``grad`` as for _rows."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous() and t.device == dev):
         _need(t, name, (dtype,), dev, n)
+    if (t.requires_grad or _forward._current_level >= 0) and not grad and _wants_more(t):
+        raise _wanted_error(t, name)
     return t.data_ptr()
 
 
@@ -1642,6 +1659,18 @@ def _fp8_out(codes, scales, rows: int, cols: int, groups: int, dev: torch.device
     return codes, scales, c, c_stride, s, s_stride
 
 
+def _given(*outputs):
+    """_overwritten for the buffers of the caller's that a call has written. All at once: a call of its own for each
+    took as long as a small operator's checks."""
+    given = [t for t in outputs if t is not None]
+    try:
+        if given:
+            torch.autograd.graph.increment_version(given)
+    except RuntimeError:  # inference tensors have no version
+        for t in given:
+            _overwritten(t)
+
+
 def fp8_quantize(x: torch.Tensor, block_rows: int = 1, codes_out: Optional[torch.Tensor] = None,
                  scales_out: Optional[torch.Tensor] = None):
     """pulse_fp8_quantize: E4M3 codes of an FP32 or BF16 matrix and the FP32 scales of its blocks of
@@ -1653,6 +1682,7 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, codes_out: Optional[torch
     dev = x.device
     codes, scales, c, c_stride, s, s_stride = _fp8_out(codes_out, scales_out, rows, cols, (rows + block_rows - 1) // block_rows, dev)
     _call("pulse_fp8_quantize", dev, src, rows, cols, stride, _TYPE_CODE[x.dtype], block_rows, c, c_stride, s, s_stride)
+    _given(codes_out, scales_out)
     return codes, scales
 
 
@@ -1679,13 +1709,10 @@ def rmsnorm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e
     if weight is not None:
         g_kind = torch.bfloat16 if isinstance(weight, torch.Tensor) and weight.dtype is torch.bfloat16 else torch.float32
         g, g_type = _vector(weight, "weight", g_kind, dev, cols), _TYPE_CODE[g_kind]
-        if weight.requires_grad and torch.is_grad_enabled():
-            raise ValueError("weight: requires a gradient, which this operator does not have (detach it, or call under no_grad)")
     codes, scales, c, c_stride, s, s_stride = _fp8_out(codes_out, scales_out, rows, cols, rows, dev)
     _call("pulse_rmsnorm_fp8", dev, src, rows, cols, stride, _TYPE_CODE[kind], res, res_stride, dst, dst_stride,
           g, g_type, eps, c, c_stride, s, s_stride)
-    if dst and (dst == src or dst == res):
-        _overwritten(total)
+    _given(codes_out, scales_out, sum_out)
     return codes, scales, total
 
 
@@ -1702,12 +1729,12 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     blocks = (k + 127) // 128
     sa, _, _, sa_stride = _rows(x_scales, "x_scales", _F32, dev, m, blocks)
     sb, _, _, sb_stride = _rows(w_scales, "w_scales", _F32, dev, (n + 127) // 128, blocks)
-    if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    dst, _, _, dst_stride = _rows(out, "out", _F32_BF16, dev, m, n)
+    dst_of = torch.empty((m, n), dtype=out_dtype, device=dev) if out is None else out
+    dst, _, _, dst_stride = _rows(dst_of, "out", _F32_BF16, dev, m, n)
     _call("pulse_fp8_linear", dev, a, m, a_stride, sa, sa_stride, b, n, b_stride, sb, sb_stride, k, dst, dst_stride,
-          _TYPE_CODE[out.dtype])
-    return out
+          _TYPE_CODE[dst_of.dtype])
+    _given(out)
+    return dst_of
 
 
 class SamplePlan:
@@ -1745,12 +1772,11 @@ class SamplePlan:
             self.device = dev
         elif dev != self.device:
             raise ValueError(f"logits: on {dev}, expected {self.device}")
-        u = _vector(uniform, "uniform", torch.float32, dev, rows)
-        if tokens_out is None:
-            tokens_out = torch.empty(rows, dtype=torch.int32, device=dev)
-        t = _vector(tokens_out, "tokens_out", torch.int32, dev, rows)
-        if logprobs_out is None and logprobs:
-            logprobs_out = torch.empty(rows, dtype=torch.float32, device=dev)
-        lp = 0 if logprobs_out is None else _vector(logprobs_out, "logprobs_out", torch.float32, dev, rows)
+        u = _vector(uniform, "uniform", torch.float32, dev, rows, grad=True)
+        new = torch.empty(rows, dtype=torch.int32, device=dev) if tokens_out is None else tokens_out
+        t = _vector(new, "tokens_out", torch.int32, dev, rows)
+        logp = torch.empty(rows, dtype=torch.float32, device=dev) if logprobs_out is None and logprobs else logprobs_out
+        lp = 0 if logp is None else _vector(logp, "logprobs_out", torch.float32, dev, rows)
         _call("pulse_sample", dev, self._ref, rows, src, stride, _TYPE_CODE[logits.dtype], u, t, lp)
-        return tokens_out, logprobs_out
+        _given(tokens_out, logprobs_out)
+        return new, logp
