@@ -957,7 +957,8 @@ int pulse_logits_sorts(const pulse_logits_shaping *shaping, uint64_t rows, int b
  * an infinity has a NaN scale and codes 0x7F. Scales are stored as
  * ceil(rows / block_rows) rows of ceil(cols / 128) floats.
  *
- * Rows of every matrix are `stride` elements apart (>= cols). Pointers are
+ * Rows of every matrix are `stride` elements apart (>= cols, below 2^40; (rows - 1)
+ * of them below 2^56: PULSE_ERR_INVALID). Pointers are
  * aligned to their element type; 16-byte aligned rows are read and written
  * fastest. Inputs and outputs share no bytes, strides and the gaps between
  * rows included, unless a call says so. Gaps are left as they are.

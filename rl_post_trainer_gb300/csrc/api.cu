@@ -1970,13 +1970,16 @@ namespace {
 
 constexpr uint64_t kMaxSide = 1ull << 31;   // rows and columns of a matrix
 constexpr uint64_t kMaxPitch = 1ull << 40;  // elements between rows
+constexpr uint64_t kMaxSpan = 1ull << 56;   // elements from the first row's begin to the last one's: ends do not wrap
 
 // A matrix's address range, from its first element to its last.
 struct Matrix {
   const void* p;
   uint64_t rows, cols, stride;
   uint64_t bytes;  // of an element
-  bool ok() const { return p != nullptr && stride >= cols && stride < kMaxPitch && aligned(p, uintptr_t(bytes)); }
+  bool ok() const {
+    return p != nullptr && stride >= cols && stride < kMaxPitch && rows - 1 < kMaxSpan / stride && aligned(p, uintptr_t(bytes));
+  }
   uint64_t begin() const { return reinterpret_cast<uintptr_t>(p); }
   uint64_t end() const { return begin() + ((rows - 1) * stride + cols) * bytes; }
   bool rows_on(uint64_t a) const { return aligned(p, uintptr_t(a)) && (rows == 1 || stride * bytes % a == 0); }
