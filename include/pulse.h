@@ -1066,6 +1066,23 @@ int pulse_debug_encode_orphan_tile(const float *master_f32, uint16_t *prev_bf16,
                                    uint32_t *idx_out, uint16_t *val_out, uint64_t *count_out,
                                    uint64_t wait_limit_ns, cudaStream_t stream);
 
+/*
+ * Test hook for the waits of the FP8 product (not for production use). Runs
+ * pulse_fp8_linear with a wait limit of `wait_limit_ns` nanoseconds (at most 1e9)
+ * while loaders of every CTA end before loading their block number `block`: bit 0
+ * of `loaders` those of the activations, bit 1 of the weights, bits 2 and 3 the
+ * same of the odd CTAs of a cluster. Expected outcome where there is such a
+ * block: the waits give up, PULSE_ERR_TIMEOUT is recorded, every write stays
+ * inside of `out`, and the next call is right; else what pulse_fp8_linear gives.
+ */
+int pulse_debug_fp8_linear_withheld(const uint8_t *x, uint64_t rows, uint64_t x_stride,
+                                    const float *x_scales, uint64_t x_scales_stride,
+                                    const uint8_t *w, uint64_t out_features, uint64_t w_stride,
+                                    const float *w_scales, uint64_t w_scales_stride,
+                                    uint64_t in_features, void *out, uint64_t out_stride,
+                                    int out_type, uint32_t loaders, uint32_t block,
+                                    uint64_t wait_limit_ns, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

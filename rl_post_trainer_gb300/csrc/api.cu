@@ -2011,6 +2011,48 @@ int stream_error_word(int device, cudaStream_t stream, uint32_t** word) {
   }
 }
 
+int fp8_linear_impl(const uint8_t* x, uint64_t rows, uint64_t x_stride, const float* x_scales, uint64_t x_scales_stride,
+                    const uint8_t* w, uint64_t out_features, uint64_t w_stride, const float* w_scales,
+                    uint64_t w_scales_stride, uint64_t in_features, void* out, uint64_t out_stride, int out_type,
+                    uint64_t wait_ns, uint32_t withheld_by, uint32_t withheld, cudaStream_t stream) {
+  if (!type_ok(out_type) || in_features == 0) return PULSE_ERR_INVALID;
+  if (rows == 0 || out_features == 0) return PULSE_OK;
+  if (rows >= kMaxSide || out_features >= kMaxSide || in_features >= kMaxSide) return PULSE_ERR_RANGE;
+  const uint64_t blocks = div_up(in_features, PULSE_FP8_BLOCK);
+  const Matrix mx{x, rows, in_features, x_stride, 1}, mw{w, out_features, in_features, w_stride, 1};
+  const Matrix sx{x_scales, rows, blocks, x_scales_stride, 4};
+  const Matrix sw{w_scales, div_up(out_features, PULSE_FP8_BLOCK), blocks, w_scales_stride, 4};
+  const Matrix dst{out, rows, out_features, out_stride, elem_bytes(out_type)};
+  if (!mx.ok() || !mw.ok() || !sx.ok() || !sw.ok() || !dst.ok() || !mx.rows_on(16) || !mw.rows_on(16))
+    return PULSE_ERR_INVALID;
+  if (!apart(dst, mx) || !apart(dst, mw) || !apart(dst, sx) || !apart(dst, sw)) return PULSE_ERR_INVALID;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
+  Fp8LinearArgs a{};
+  a.x = x;
+  a.w = w;
+  a.x_scales = x_scales;
+  a.w_scales = w_scales;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.w_stride = w_stride;
+  a.x_scales_stride = x_scales_stride;
+  a.w_scales_stride = w_scales_stride;
+  a.out_stride = out_stride;
+  a.rows = uint32_t(rows);
+  a.n = uint32_t(out_features);
+  a.k = uint32_t(in_features);
+  a.blocks = uint32_t(blocks);
+  a.out_bf16 = out_type == PULSE_BF16;
+  a.out_vec = dst.rows_on(16);
+  a.wait_ns = wait_ns;
+  a.withheld_by = withheld_by;
+  a.withheld = withheld;
+  const int st = stream_error_word(device, stream, &a.error_word);
+  if (st != PULSE_OK) return st;
+  return launch_fp8_linear(a, sm_count(device), stream);
+}
+
 }  // namespace
 
 int pulse_fp8_quantize(const void* x, uint64_t rows, uint64_t cols, uint64_t stride, int type, int block_rows,
@@ -2087,39 +2129,18 @@ int pulse_fp8_linear(const uint8_t* x, uint64_t rows, uint64_t x_stride, const f
                      uint64_t x_scales_stride, const uint8_t* w, uint64_t out_features, uint64_t w_stride,
                      const float* w_scales, uint64_t w_scales_stride, uint64_t in_features, void* out,
                      uint64_t out_stride, int out_type, cudaStream_t stream) {
-  if (!type_ok(out_type) || in_features == 0) return PULSE_ERR_INVALID;
-  if (rows == 0 || out_features == 0) return PULSE_OK;
-  if (rows >= kMaxSide || out_features >= kMaxSide || in_features >= kMaxSide) return PULSE_ERR_RANGE;
-  const uint64_t blocks = div_up(in_features, PULSE_FP8_BLOCK);
-  const Matrix mx{x, rows, in_features, x_stride, 1}, mw{w, out_features, in_features, w_stride, 1};
-  const Matrix sx{x_scales, rows, blocks, x_scales_stride, 4};
-  const Matrix sw{w_scales, div_up(out_features, PULSE_FP8_BLOCK), blocks, w_scales_stride, 4};
-  const Matrix dst{out, rows, out_features, out_stride, elem_bytes(out_type)};
-  if (!mx.ok() || !mw.ok() || !sx.ok() || !sw.ok() || !dst.ok() || !mx.rows_on(16) || !mw.rows_on(16))
-    return PULSE_ERR_INVALID;
-  if (!apart(dst, mx) || !apart(dst, mw) || !apart(dst, sx) || !apart(dst, sw)) return PULSE_ERR_INVALID;
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess) return PULSE_ERR_CUDA;
-  Fp8LinearArgs a{};
-  a.x = x;
-  a.w = w;
-  a.x_scales = x_scales;
-  a.w_scales = w_scales;
-  a.out = out;
-  a.x_stride = x_stride;
-  a.w_stride = w_stride;
-  a.x_scales_stride = x_scales_stride;
-  a.w_scales_stride = w_scales_stride;
-  a.out_stride = out_stride;
-  a.rows = uint32_t(rows);
-  a.n = uint32_t(out_features);
-  a.k = uint32_t(in_features);
-  a.blocks = uint32_t(blocks);
-  a.out_bf16 = out_type == PULSE_BF16;
-  a.out_vec = dst.rows_on(16);
-  const int st = stream_error_word(device, stream, &a.error_word);
-  if (st != PULSE_OK) return st;
-  return launch_fp8_linear(a, sm_count(device), stream);
+  return fp8_linear_impl(x, rows, x_stride, x_scales, x_scales_stride, w, out_features, w_stride, w_scales, w_scales_stride,
+                         in_features, out, out_stride, out_type, kDefaultWaitNs, 0u, 0u, stream);
+}
+
+int pulse_debug_fp8_linear_withheld(const uint8_t* x, uint64_t rows, uint64_t x_stride, const float* x_scales,
+                                    uint64_t x_scales_stride, const uint8_t* w, uint64_t out_features, uint64_t w_stride,
+                                    const float* w_scales, uint64_t w_scales_stride, uint64_t in_features, void* out,
+                                    uint64_t out_stride, int out_type, uint32_t loaders, uint32_t block,
+                                    uint64_t wait_limit_ns, cudaStream_t stream) {
+  if (loaders == 0 || loaders > 15 || wait_limit_ns > kDefaultWaitNs) return PULSE_ERR_INVALID;
+  return fp8_linear_impl(x, rows, x_stride, x_scales, x_scales_stride, w, out_features, w_stride, w_scales, w_scales_stride,
+                         in_features, out, out_stride, out_type, wait_limit_ns, loaders, block, stream);
 }
 
 int pulse_sample(const pulse_sampling* sampling, uint64_t rows, const void* logits, uint64_t stride, int type,

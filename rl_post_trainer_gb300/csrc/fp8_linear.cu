@@ -21,7 +21,9 @@
 // products alone take 207 us, with the loads 276, with the hand-over of TMEM's two slots, nothing read, 387.
 //
 // Warps: 0 and 2 load (one thread each), 1 and 3 issue products (one thread each), the others are the epilogue.
-// Every wait has a time limit; one that runs out records PULSE_ERR_TIMEOUT and ends the CTA.
+// Every wait has a time limit; one that runs out records PULSE_ERR_TIMEOUT and ends the roles one after the other. A CTA leaves
+// with nothing under way into its memory: the loaders wait for the last products to let go of their stages (what arrives there
+// last); after a wait that ran out, one thread goes by the counts of what each role has begun.
 #include <atomic>
 
 #include "pulse.h"
@@ -32,8 +34,23 @@ namespace pulse {
 namespace {
 
 constexpr uint32_t kLanes = 128, kBlock = 128;
-constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kLaneTile = kLanes * kBlock;  // bytes of the lane side's tile
+
+__device__ __forceinline__ bool withholds(const Fp8LinearArgs& a, uint32_t rank, bool weights, uint32_t block) {
+  return block == a.withheld && (a.withheld_by >> (2 * (rank & 1u) + (weights ? 1u : 0u)) & 1u);
+}
+// After a wait that ran out: the arrivals of the products that the two issuers, each with every other block, have begun.
+template <uint32_t kStages, uint32_t kSlots>
+__device__ __forceinline__ void settle_products(const uint32_t* issued, uint64_t* empty, uint64_t* tmem_full, uint64_t limit_ns) {
+  for (uint32_t q = 0; q < 2; ++q) {
+    const uint32_t n = issued[q];
+    for (uint32_t d = n > kStages / 2 ? n - kStages / 2 : 0; d < n; ++d) {
+      const uint32_t b = q + 2 * d;
+      mbar_wait_often(&empty[b % kStages], (b / kStages) & 1u, limit_ns);
+      if (d + kSlots / 2 >= n) mbar_wait_often(&tmem_full[b % kSlots], (b / kSlots) & 1u, limit_ns);
+    }
+  }
+}
 
 struct Work {
   uint32_t lane_tiles, col_tiles;
@@ -157,6 +174,8 @@ constexpr uint32_t kPairFew = 40, kPairMany = 232;  // registers of the first fo
 struct PairBars {
   uint64_t full[kPairStages], empty[kPairStages], tmem_full[kPairSlots], tmem_empty[kPairSlots];
   uint32_t tmem, stop;
+  uint32_t loaded[4];  // blocks that the loaders have begun, of the even CTA's tokens, weights, of the odd one's (in the even CTA)
+  uint32_t issued[2];  // blocks that the issuers have (in both)
 };
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -187,9 +206,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
   volatile uint32_t* stop = &bars.stop;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*stop == 0 && mbar_wait_often(bar, parity, kWaitNs)) return true;
+    if (*stop == 0 && mbar_wait_often(bar, parity, a.wait_ns)) return true;
     if (*stop == 0) record_error(a.error_word, kErrTimeout);
     *stop = 1;
+    peer_store(&bars.stop, rank ^ 1u, 1);
     return false;
   };
 
@@ -206,7 +226,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
       for (uint32_t t = first; t < tiles_all && live; t += step) {
         const uint32_t ct = t / work.lane_tiles, lt = t - ct * work.lane_tiles, from = (tokens ? lt : ct) * 256 + rank * 128;
         for (uint32_t b = 0; b < a.blocks; ++b) {
-          if (!(live = wait(&bars.empty[stage], phase ^ 1u))) break;
+          live = !withholds(a, rank, !tokens, loaded) && wait(&bars.empty[stage], phase ^ 1u);
+          if (!live) break;
           if (tokens && rank == 0) mbar_arrive_expect_tx(&bars.full[stage], 2 * kPairStage);
           tma_load_2d_pair(tiles + stage * kPairStage + (tokens ? 0u : kLaneTile), map, b * kBlock, from,
                            peer_addr(&bars.full[stage], 0), keep);
@@ -214,9 +235,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
           if (++stage == kPairStages) stage = 0, phase ^= 1u;
         }
       }
-      if (!live && tokens && rank == 0)  // the copies in flight end before the CTAs do
-        for (uint32_t i = loaded > kPairStages ? loaded - kPairStages : 0; i < loaded; ++i)
-          mbar_wait_often(&bars.full[i % kPairStages], (i / kPairStages) & 1u, kWaitNs);
+      for (int i = 0; i < kPairStages && live; ++i) {
+        live = wait(&bars.empty[stage], phase ^ 1u);
+        if (++stage == kPairStages) stage = 0, phase ^= 1u;
+      }
+      peer_store(&bars.loaded[2 * rank + (tokens ? 0 : 1)], 0, loaded);
     } else if ((warp & 1u) && lane == 0 && rank == 0) {
       // Two threads issue, each for one slot of TMEM: between two blocks a thread spends some 600 cycles
       // in waits and commits, longer than the products that are queued behind one another.
@@ -235,8 +258,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
         mma_commit_pair(&bars.empty[stage]);
         if ((stage += 2) >= kPairStages) stage -= kPairStages, phase ^= 1u;
       }
-      if (!live && done)  // so do the products
-        mbar_wait_often(&bars.tmem_full[slot], (done - 1) & 1u, kWaitNs);
+      for (uint32_t r = 0; r < 2; ++r) peer_store(&bars.issued[slot], r, done);
     }
   } else {
     more_registers<kPairMany>();
@@ -281,6 +303,27 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
   __syncwarp();
   tmem_fence_before();
   cluster_sync();  // no CTA leaves while the other arrives at its barriers or reads its operands
+  if (*stop != 0) {  // known to both CTAs
+    if (warp == 2 && lane == 0) {
+      if (rank == 0) {  // the copies of both CTAs arrive here
+        uint32_t most = 0;
+        for (int k = 0; k < 4; ++k) most = max(most, bars.loaded[k]);
+        for (uint32_t i = most > kPairStages ? most - kPairStages : 0; i < most; ++i) {
+          uint64_t* bar = &bars.full[i % kPairStages];
+          uint32_t bytes = 0;
+          for (int k = 0; k < 4; ++k) bytes += i < bars.loaded[k] ? kLaneTile : 0u;
+          if (i >= bars.loaded[0])
+            mbar_arrive_expect_tx(bar, bytes);
+          else if (bytes < 2 * kPairStage)
+            mbar_complete_tx(bar, 2 * kPairStage - bytes);
+          mbar_wait_often(bar, (i / kPairStages) & 1u, a.wait_ns);
+        }
+      }
+      settle_products<kPairStages, kPairSlots>(bars.issued, bars.empty, bars.tmem_full, a.wait_ns);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 2) {
     tmem_fence_after();
     tmem_free_pair(tmem, 512);
@@ -304,6 +347,7 @@ struct Narrow {
 struct NarrowBars {
   uint64_t full[16], empty[16], tmem_full[4], tmem_empty[4];
   uint32_t tmem, stop;
+  uint32_t loaded[2], issued[2];  // blocks that the loaders (tokens, weights) and the issuers have begun
 };
 
 template <int kCols>
@@ -339,7 +383,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap weight_map, const __gri
   volatile uint32_t* stop = &bars.stop;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*stop == 0 && mbar_wait_often(bar, parity, kWaitNs)) return true;
+    if (*stop == 0 && mbar_wait_often(bar, parity, a.wait_ns)) return true;
     if (*stop == 0) record_error(a.error_word, kErrTimeout);
     *stop = 1;
     return false;
@@ -354,16 +398,19 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap weight_map, const __gri
     for (uint32_t t = first; t < tiles_all && live; t += step) {  // tiles of the same weights follow one another
       const uint32_t lt = t / work.col_tiles, ct = t - lt * work.col_tiles, from = weights ? lt * kLanes : ct * kCols;
       for (uint32_t b = b0; b < b1; ++b) {
-        if (!(live = wait(&bars.empty[stage], phase ^ 1u))) break;
+        live = !withholds(a, rank, weights, loaded) && wait(&bars.empty[stage], phase ^ 1u);
+        if (!live) break;
         if (weights) mbar_arrive_expect_tx(&bars.full[stage], S::kStageBytes);
         tma_load_2d(tiles + stage * S::kStageBytes + (weights ? 0u : kLaneTile), map, b * kBlock, from, &bars.full[stage], policy);
         ++loaded;
         if (++stage == S::kStages) stage = 0, phase ^= 1u;
       }
     }
-    if (!live && weights)  // the copies in flight end before the CTA does
-      for (uint32_t i = loaded > S::kStages ? loaded - S::kStages : 0; i < loaded; ++i)
-        mbar_wait_often(&bars.full[i % S::kStages], (i / S::kStages) & 1u, kWaitNs);
+    for (int i = 0; i < S::kStages && live; ++i) {
+      live = wait(&bars.empty[stage], phase ^ 1u);
+      if (++stage == S::kStages) stage = 0, phase ^= 1u;
+    }
+    bars.loaded[weights ? 1 : 0] = loaded;
   } else if (warp < 4 && lane == 0) {  // two threads issue, each for every other slot of TMEM
     constexpr uint32_t instruction = fp8_instruction(kLanes, kCols);
     const uint32_t total = (tiles_all - first + step - 1) / step * (b1 - b0);  // first < tiles_all
@@ -382,10 +429,7 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap weight_map, const __gri
       if ((stage += 2) >= S::kStages) stage -= S::kStages, phase ^= 1u;
       if ((slot += 2) >= S::kSlots) slot -= S::kSlots, slot_phase ^= 1u;
     }
-    if (!live && done) {  // so do the products
-      const uint32_t last = (warp >> 1) + 2 * (done - 1);
-      mbar_wait_often(&bars.tmem_full[last % S::kSlots], (last / S::kSlots) & 1u, kWaitNs);
-    }
+    bars.issued[warp >> 1] = done;
   } else if (warp >= 4) {
     const uint32_t me = threadIdx.x - 128u, quarter = warp & 3u, row = quarter * 32u + lane;
     const uint32_t col0 = (warp - 4u) / 4u * S::kWarpCols;  // first of the warp's columns
@@ -484,6 +528,19 @@ linear_narrow_kernel(const __grid_constant__ CUtensorMap weight_map, const __gri
   tmem_fence_before();
   __syncthreads();
   if (warp == 2) {
+    if (lane == 0 && *stop != 0) {
+      const uint32_t tokens = bars.loaded[0], weights = bars.loaded[1], most = max(tokens, weights);
+      for (uint32_t i = most > S::kStages ? most - S::kStages : 0; i < most; ++i) {
+        uint64_t* bar = &bars.full[i % S::kStages];
+        if (i >= weights)
+          mbar_arrive_expect_tx(bar, kCols * kBlock);
+        else if (i >= tokens)
+          mbar_complete_tx(bar, kCols * kBlock);
+        mbar_wait_often(bar, (i / S::kStages) & 1u, a.wait_ns);
+      }
+      settle_products<S::kStages, S::kSlots>(bars.issued, bars.empty, bars.tmem_full, a.wait_ns);
+    }
+    __syncwarp();
     tmem_fence_after();
     tmem_free(tmem, S::kTmemCols);
   }

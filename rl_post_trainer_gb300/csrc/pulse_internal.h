@@ -503,6 +503,9 @@ struct Fp8LinearArgs {
   bool out_bf16;
   bool out_vec;             // rows of out begin at multiples of 16 bytes
   uint32_t* error_word;
+  uint64_t wait_ns;         // limit of every wait
+  // Test hook: these loaders of a CTA (bit 0: tokens, 1: weights; 2 and 3: of the odd CTAs of a cluster) end before this block.
+  uint32_t withheld_by, withheld;
 };
 int launch_fp8_linear(const Fp8LinearArgs& a, int sms, cudaStream_t stream);  // a status code
 

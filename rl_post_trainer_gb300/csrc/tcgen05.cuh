@@ -116,6 +116,10 @@ __device__ __forceinline__ void tmem_read(unsigned long long (&v)[8], uint32_t a
       : "r"(address)
       : "memory");
 }
+// What a copy of `bytes` that never came would have signalled.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
 // Bounded wait for phase `parity` of `bar` that looks at the clock every 64 tries only, so that the reads of the global
 // timer stay out of short waits (no difference was measured: a try suspends the thread for a while itself).
 __device__ __forceinline__ bool mbar_wait_often(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -125,7 +129,7 @@ __device__ __forceinline__ bool mbar_wait_often(uint64_t* bar, uint32_t parity, 
     if ((it & 63u) == 0) {
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > limit_ns) return false;
+      if (now - t0 > limit_ns) return mbar_try_wait(bar, parity);  // the time may have gone by while nothing of the GPU's ran
     }
   }
   return false;
@@ -152,6 +156,9 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(p, rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

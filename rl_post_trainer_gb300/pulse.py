@@ -288,6 +288,8 @@ def lib():
             "pulse_fp8_quantize": ([P, U64, U64, U64, I, I, P, U64, P, U64, P], I),
             "pulse_rmsnorm_fp8": ([P, U64, U64, U64, I, P, U64, P, U64, P, I, ctypes.c_float, P, U64, P, U64, P], I),
             "pulse_fp8_linear": ([P, U64, U64, P, U64, P, U64, U64, P, U64, U64, P, U64, I, P], I),
+            "pulse_debug_fp8_linear_withheld": ([P, U64, U64, P, U64, P, U64, U64, P, U64, U64, P, U64, I, ctypes.c_uint32,
+                                                 ctypes.c_uint32, U64, P], I),
             "pulse_sample": ([ctypes.POINTER(PulseSampling), U64, P, U64, I, P, P, P, P], I),
             "pulse_logits_sorts": ([ctypes.POINTER(PulseLogitsShaping), U64, I, ctypes.POINTER(I)], I),
         }
@@ -1735,6 +1737,13 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
           _TYPE_CODE[dst_of.dtype])
     _given(out)
     return dst_of
+
+
+def debug_fp8_linear_withheld(x, x_scales, w, w_scales, out, loaders: int, block: int, wait_limit_ns: int):
+    """Test hook for the product's waits (see include/pulse.h)."""
+    _call("pulse_debug_fp8_linear_withheld", x.device, x.data_ptr(), x.shape[0], x.stride(0), x_scales.data_ptr(), x_scales.stride(0),
+          w.data_ptr(), w.shape[0], w.stride(0), w_scales.data_ptr(), w_scales.stride(0), x.shape[1], out.data_ptr(), out.stride(0),
+          _TYPE_CODE[out.dtype], loaders, block, wait_limit_ns)
 
 
 class SamplePlan:
