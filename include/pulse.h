@@ -1071,7 +1071,8 @@ int pulse_debug_encode_orphan_tile(const float *master_f32, uint16_t *prev_bf16,
  * pulse_fp8_linear with a wait limit of `wait_limit_ns` nanoseconds (at most 1e9)
  * while loaders of every CTA end before loading their block number `block`: bit 0
  * of `loaders` those of the activations, bit 1 of the weights, bits 2 and 3 the
- * same of the odd CTAs of a cluster. Expected outcome where there is such a
+ * same of the odd CTAs of a cluster; bit 4: many tokens go the way that is taken
+ * where pairs of CTAs cannot be had. Expected outcome where there is such a
  * block: the waits give up, PULSE_ERR_TIMEOUT is recorded, every write stays
  * inside of `out`, and the next call is right; else what pulse_fp8_linear gives.
  */

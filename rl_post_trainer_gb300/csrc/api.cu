@@ -2014,7 +2014,7 @@ int stream_error_word(int device, cudaStream_t stream, uint32_t** word) {
 int fp8_linear_impl(const uint8_t* x, uint64_t rows, uint64_t x_stride, const float* x_scales, uint64_t x_scales_stride,
                     const uint8_t* w, uint64_t out_features, uint64_t w_stride, const float* w_scales,
                     uint64_t w_scales_stride, uint64_t in_features, void* out, uint64_t out_stride, int out_type,
-                    uint64_t wait_ns, uint32_t withheld_by, uint32_t withheld, cudaStream_t stream) {
+                    uint64_t wait_ns, uint32_t withheld_by, uint32_t withheld, bool pairs, cudaStream_t stream) {
   if (!type_ok(out_type) || in_features == 0) return PULSE_ERR_INVALID;
   if (rows == 0 || out_features == 0) return PULSE_OK;
   if (rows >= kMaxSide || out_features >= kMaxSide || in_features >= kMaxSide) return PULSE_ERR_RANGE;
@@ -2050,7 +2050,7 @@ int fp8_linear_impl(const uint8_t* x, uint64_t rows, uint64_t x_stride, const fl
   a.withheld = withheld;
   const int st = stream_error_word(device, stream, &a.error_word);
   if (st != PULSE_OK) return st;
-  return launch_fp8_linear(a, sm_count(device), stream);
+  return launch_fp8_linear(a, sm_count(device), pairs, stream);
 }
 
 }  // namespace
@@ -2130,7 +2130,7 @@ int pulse_fp8_linear(const uint8_t* x, uint64_t rows, uint64_t x_stride, const f
                      const float* w_scales, uint64_t w_scales_stride, uint64_t in_features, void* out,
                      uint64_t out_stride, int out_type, cudaStream_t stream) {
   return fp8_linear_impl(x, rows, x_stride, x_scales, x_scales_stride, w, out_features, w_stride, w_scales, w_scales_stride,
-                         in_features, out, out_stride, out_type, kDefaultWaitNs, 0u, 0u, stream);
+                         in_features, out, out_stride, out_type, kDefaultWaitNs, 0u, 0u, true, stream);
 }
 
 int pulse_debug_fp8_linear_withheld(const uint8_t* x, uint64_t rows, uint64_t x_stride, const float* x_scales,
@@ -2138,9 +2138,9 @@ int pulse_debug_fp8_linear_withheld(const uint8_t* x, uint64_t rows, uint64_t x_
                                     const float* w_scales, uint64_t w_scales_stride, uint64_t in_features, void* out,
                                     uint64_t out_stride, int out_type, uint32_t loaders, uint32_t block,
                                     uint64_t wait_limit_ns, cudaStream_t stream) {
-  if (loaders == 0 || loaders > 15 || wait_limit_ns > kDefaultWaitNs) return PULSE_ERR_INVALID;
+  if (loaders == 0 || loaders > 31 || wait_limit_ns > kDefaultWaitNs) return PULSE_ERR_INVALID;
   return fp8_linear_impl(x, rows, x_stride, x_scales, x_scales_stride, w, out_features, w_stride, w_scales, w_scales_stride,
-                         in_features, out, out_stride, out_type, wait_limit_ns, loaders, block, stream);
+                         in_features, out, out_stride, out_type, wait_limit_ns, loaders & 15u, block, !(loaders & 16u), stream);
 }
 
 int pulse_sample(const pulse_sampling* sampling, uint64_t rows, const void* logits, uint64_t stride, int type,

@@ -213,7 +213,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap token_map, const __grid_c
     return false;
   };
 
-  // 384 threads of 168 registers become 128 of 40 and 256 of 232 (the host has checked that these are not more)
+  // 384 threads of 168 registers become 128 of 40 and 256 of 232 (pairs_fit: these are not more)
   if (warp < 4) {
     fewer_registers<kPairFew>();
     if ((warp & 1u) == 0 && lane == 0) {
@@ -552,15 +552,17 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeTiled encode_tiled() {
-  static const EncodeTiled f = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
+EncodeTiled encode_tiled() {  // asked for again where it was not to be had
+  static std::atomic<EncodeTiled> known{nullptr};
+  EncodeTiled f = known.load(std::memory_order_acquire);
+  if (f != nullptr) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiled>(p);
+  known.store(f, std::memory_order_release);
   return f;
 }
 
@@ -605,15 +607,22 @@ int launch(K kernel, uint32_t ctas, uint32_t threads, uint32_t bytes, uint32_t c
   return cudaLaunchKernelEx(&c, kernel, first, second, a, w) == cudaSuccess ? PULSE_OK : PULSE_ERR_CUDA;
 }
 
+// Whether the pair kernel was compiled with the registers that its warps share out anew: more than the launch has would be
+// waited for without end. 168 a thread are just enough; a compiler that gives it fewer leaves it out.
+bool pairs_fit() {
+  static std::atomic<int> known{0};
+  int registers = known.load(std::memory_order_relaxed);
+  if (registers == 0) {
+    cudaFuncAttributes f{};
+    if (cudaFuncGetAttributes(&f, linear_pair_kernel) != cudaSuccess) return false;
+    known.store(registers = f.numRegs, std::memory_order_relaxed);
+  }
+  return registers * kPairThreads >= int(128 * kPairFew + 32 * kPairWarps * kPairMany);
+}
+
 int launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
   if (!allow_shared(reinterpret_cast<const void*>(linear_pair_kernel), kPairBytes, ready)) return PULSE_ERR_CUDA;
-  // more registers than the launch has would be waited for without end
-  static const int registers = [] {
-    cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, linear_pair_kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (registers * kPairThreads < int(128 * kPairFew + 32 * kPairWarps * kPairMany)) return PULSE_ERR_CUDA;
   CUtensorMap tokens, weights;
   if (!make_map(&tokens, a.x, a.rows, a.k, a.x_stride, 128) || !make_map(&weights, a.w, a.n, a.k, a.w_stride, 128))
     return PULSE_ERR_CUDA;
@@ -652,12 +661,12 @@ int launch_narrow(const Fp8LinearArgs& a, int sms, cudaStream_t stream) {
 // at most; where even those of 128 columns do not, the pair's, which read half as much for a product (4096 columns into n
 // outputs, us with 64, 128, pair: 256 tokens, n = 4096 12.2, 15.0, 20.6; n = 9728 21.6, 19.1, 21.1; n = 14336 30.8, 34.9, 21.7;
 // 512 tokens, n = 2048 12.0, 14.8, 20.5; n = 4096 21.4, 18.7, 20.7; n = 9728 39.9, 34.6, 21.7).
-int launch_fp8_linear(const Fp8LinearArgs& a, int sms, cudaStream_t stream) {
+int launch_fp8_linear(const Fp8LinearArgs& a, int sms, bool pairs, cudaStream_t stream) {
   auto tiles = [&](uint32_t cols) { return uint64_t((a.rows + cols - 1) / cols) * ((a.n + kLanes - 1) / kLanes); };
   if (a.rows <= 16) return launch_narrow<16>(a, sms, stream);
   if (a.rows <= 32) return launch_narrow<32>(a, sms, stream);
   if (a.rows <= 64 || tiles(64) <= uint64_t(sms)) return launch_narrow<64>(a, sms, stream);
-  if (a.rows <= 128 || tiles(128) <= uint64_t(sms)) return launch_narrow<128>(a, sms, stream);
+  if (a.rows <= 128 || tiles(128) <= uint64_t(sms) || !pairs || !pairs_fit()) return launch_narrow<128>(a, sms, stream);
   return launch_pair(a, sms, stream);
 }
 

@@ -507,7 +507,8 @@ struct Fp8LinearArgs {
   // Test hook: these loaders of a CTA (bit 0: tokens, 1: weights; 2 and 3: of the odd CTAs of a cluster) end before this block.
   uint32_t withheld_by, withheld;
 };
-int launch_fp8_linear(const Fp8LinearArgs& a, int sms, cudaStream_t stream);  // a status code
+// A status code. `pairs`: whether pairs of CTAs may be taken.
+int launch_fp8_linear(const Fp8LinearArgs& a, int sms, bool pairs, cudaStream_t stream);
 
 struct SampleArgs {
   const void* logits;

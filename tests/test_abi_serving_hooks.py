@@ -13,6 +13,6 @@ def test_withheld_arguments():
 
     def call(loaders=1, limit=1000, m=4, xs=320):
         return pulse.lib().pulse_debug_fp8_linear_withheld(P(A), m, xs, P(B), 3, P(C), 200, 320, P(D), 3, 300, P(F), 200, 0, loaders, 0, limit, P(0))
-    for bad in (dict(loaders=0), dict(loaders=16), dict(limit=1_000_000_001), dict(xs=312)):
+    for bad in (dict(loaders=0), dict(loaders=32), dict(limit=1_000_000_001), dict(xs=312)):
         assert call(**bad) == pulse.pulse.PULSE_ERR_INVALID, bad
     assert call(m=0) == pulse.pulse.PULSE_OK

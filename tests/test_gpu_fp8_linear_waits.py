@@ -70,3 +70,21 @@ def test_another_stream_goes_on():
     with torch.cuda.stream(streams[1]):
         assert pulse.get_error() == E.PULSE_OK
     assert all(torch.equal(want, g) for g in got)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,k,n", [(129, 1000, 10001), (400, 2003, 5003), (2049, 128, 1281), (513, 5000, 4000), (3000, 300, 20011)])
+def test_many_tokens_without_pairs(m, k, n, dtype):
+    """What a build whose pair kernel has too few registers does instead."""
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    c, s = codes_of(m, k, 1, 1, wild=m % 2 == 1)
+    w, sw = codes_of(n, k, 2, 128)
+    for pitch, shift in ((n, 0), (n + 3, 1)):
+        out = Rows(m, n, dtype, pitch, shift)
+        x_c, w_c, x_s, w_s = on_gpu(c, (k + 31) // 16 * 16), on_gpu(w), torch.from_numpy(s).cuda(), torch.from_numpy(sw).cuda()
+        E.debug_fp8_linear_withheld(x_c, x_s, w_c, w_s, out.t, 16, 0, 1_000_000_000)
+        torch.cuda.synchronize()
+        check_product(c, s, w, sw, out.t, dtype)
+        out.check()
+    assert pulse.get_error() == E.PULSE_OK
