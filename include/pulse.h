@@ -1022,13 +1022,15 @@ int pulse_fp8_linear(const uint8_t *x, uint64_t rows, uint64_t x_stride, const f
  *   top-k   the first top_k[r] tokens                    (<= 0: all)
  *   top-p   of those, the ones before which less than top_p[r] of their mass
  *           lies, one at least                           (not below 1: all)
- *   min-p   tokens with w >= min_p[r]; the likeliest always (not above 0: all)
+ *   min-p   tokens with w >= min_p[r]                    (not above 0: all;
+ *           1 and more: those of the largest logit)
  *   token = the lowest t such that the w of the kept tokens 0..t sum to more
  *           than uniform[r] times the w of all kept ones
  *   T not above 0: the lowest token with the largest logit, whatever the rest says
+ *   T in (0, 2^-127) counts as 2^-127; at an infinite T all finite logits weigh 1
  *   logprob = (x[token] - max x) / T - log(sum of w over the whole row), with
  *           T = 1 where it is not above 0
- * w is computed to about 2^-44, sums and comparisons are exact on whole
+ * w is computed to about 2^-44 (T up to 2^100), sums and comparisons are exact on whole
  * multiples of 2^-47 (2^-(62 - log2 of the vocabulary) for large ones): a token
  * less likely than that has no share. logprob is FP32, its sum of w off by 2^-18
  * at most. Differences x - max x are FP32 numbers: past its range they count as

@@ -49,6 +49,7 @@ constexpr uint32_t kList = 1536;                  // tokens of a list
 constexpr uint32_t kSliceBytes = 32 * 1024;
 constexpr uint32_t kSliceMost = 180 * 1024;       // more than that stays in global memory
 constexpr uint32_t kCtas = 16;                    // of a cluster
+constexpr float kLeastT = 0x1p-127f;              // log2(e) over less is no FP32 number
 
 // 2^(j / 64) * 2^47, rounded to nearest
 __device__ const unsigned long long kExp2[64] = {
@@ -762,9 +763,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a, uint3
     cluster.post(sh.bounds, bound);
   }
   if (cluster.rank == 0 && warp == kWarps - 1 && lane < ctas) {
-    const float t = greedy ? 1.0f : s.t, ch = fminf(__fdiv_rn(kLog2EHi, t), 3.4028234e38f);  // log2(e) / T as a sum of two floats
+    const float t = greedy ? 1.0f : fmaxf(s.t, kLeastT), ch = __fdiv_rn(kLog2EHi, t);  // log2(e) / T as a sum of two floats
     const float cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-ch, t, kLog2EHi), kLog2ELo), t);
-    cluster.store(&sh.t, lane, s.t);
+    cluster.store(&sh.t, lane, greedy ? s.t : t);
     cluster.store(&sh.p, lane, s.p);
     cluster.store(&sh.u, lane, s.u);
     cluster.store(&sh.min_p, lane, min_p);
