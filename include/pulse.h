@@ -1000,7 +1000,9 @@ int pulse_rmsnorm_fp8(const void *x, uint64_t rows, uint64_t cols, uint64_t stri
  * (block_rows 128):
  *   out[m][n] = sum over blocks b of x_scales[m][b] * w_scales[n / 128][b] *
  *               (sum over k in b of x[m][k] * w[n][k])
- * with FP32 sums, rounded once to out_type (PULSE_F32 or PULSE_BF16). Results
+ * with FP32 sums, rounded once to out_type (PULSE_F32 or PULSE_BF16). The two
+ * scales are multiplied first, in FP32: a product past its range is infinite or 0,
+ * one below 2^-126 has fewer bits. Results
  * are the same bits for the same inputs, sizes and device; the number of rows of a call
  * decides how its sums are ordered. NaN codes give NaN.
  *   x  rows x in_features codes, w  out_features x in_features codes: both
