@@ -37,7 +37,7 @@ constexpr float kSmallScale = 0x1p-90f, kLift = 0x1p64f;
 // of four. Packed: a run in 16 or 8 lanes, a lane's columns in a row, for matrices whose rows begin at
 // multiples of 16 bytes. Loose, for all others: a run in 32 lanes, lane i columns i, i + 32, i + 64,
 // i + 96, so that a warp's accesses of single elements lie side by side (333 x 5003 FP32 through
-// the norm: 8 us; with 8 columns in a row a lane, 30 us), none of them behind a branch, so that all are under way at once.
+// the norm: 6 us; with 8 columns in a row a lane, 30 us), none of them behind a branch, so that all are under way at once.
 // What a run costs beside its elements (scale, reciprocal,
 // maximum, addresses) is most of the instructions: 16 values a lane instead of 8 took the embedding's BF16 view of
 // 151936 x 1536 from 149 to 104 us, arithmetic by pairs 16384 x 8960 from 78 to 73 us. Values are kept as they are read until they are needed.

@@ -15,9 +15,9 @@
 //  * tokens on the lanes, 256 weight rows on the columns, for many: a lane has one scale a
 //    block, kept in a register.
 //
-// Measured: one token, 1536 into 8960 6.5 us (13.8 MB: 2.0 us of copy; the launch, one block's way through and the joining
-// of the parts are the rest), 4096 into 14336 12.1; 64 tokens, 1536 into 151936 38.7 us, 6.5 TB/s of the copy's 6.8; 8192 tokens,
-// 4096 into 14336 410 to 432 us, 2.23 to 2.35 PFLOP/s, bound by the way of a block's sums between products and epilogue: the
+// Measured: one token, 1536 into 8960 6.9 us (13.8 MB: 2.0 us of copy; the launch, one block's way through and the joining
+// of the parts are the rest), 4096 into 14336 12.5; 64 tokens, 1536 into 151936 39.8 us, 6.4 TB/s of the copy's 6.8; 8192 tokens,
+// 4096 into 14336 408 to 434 us, 2.22 to 2.36 PFLOP/s, bound by the way of a block's sums between products and epilogue: the
 // products alone take 207 us, with the loads 276, with the hand-over of TMEM's two slots, nothing read, 387.
 //
 // Warps: 0 and 2 load (one thread each), 1 and 3 issue products (one thread each), the others are the epilogue.

@@ -25,9 +25,9 @@
 // more than one answer (a number within 2^-18 of the total from a border between two tokens, a
 // nucleus whose last token it could change) they are taken again with exp_fixed, ten times the work.
 //
-// Measured (us; top-k 50, no cut, top-p 0.9 of a flat row, whose nucleus are tens of thousands of tokens): a row of 151936 FP32
-// 11, 12, 38; 256 rows of 128256 BF16 57, 81, 253 (the bytes alone 10); 2001 rows of 32003 FP32 171, 162, 431 (the bytes
-// alone 38). Not memory bounds it (13 % of DRAM's cycles with top-k) but the chain of a CTA: load, largest, bound, list, search or
+// Measured (us; top-k 50, no cut, top-p 0.9 of a flat row, whose nucleus are tens of thousands of tokens, greedy): a row of 151936
+// FP32 10, 8, 33, 6; 256 rows of 128256 BF16 57, 79, 255, 40 (the bytes alone 10); 2001 rows of 32003 FP32 169, 161, 432, 118 (the
+// bytes alone 38). Not memory bounds it (13 % of DRAM's cycles with top-k) but the chain of a CTA: load, largest, bound, list, search or
 // draw, each behind a barrier of the cluster; with a cut in a flat row the instructions of exp_fixed.
 #include <atomic>
 #include <type_traits>
