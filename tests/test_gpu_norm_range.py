@@ -26,10 +26,8 @@ def test_small_and_large_rows(cols, dtype):
         pytest.fail("CUDA device required for -m gpu tests")
     x = rows_of(cols, dtype, cols)
     g = 1 + 0.1 * torch.randn(cols, generator=torch.Generator().manual_seed(1))
-    small = x[:6]
     for eps in (0.0, 1e-44, 1e-38, 1e-30, 1e-12):
-        rows = x if eps == 0.0 else torch.cat([small, x[6:]])
-        check_norm(rows, None, g, float(np.float32(eps)), pulse.rmsnorm_fp8(rows.cuda(), g.cuda(), eps), dtype)
+        check_norm(x, None, g, float(np.float32(eps)), pulse.rmsnorm_fp8(x.cuda(), g.cuda(), eps), dtype)
     # halves that add up to the row, in place and off 16 bytes
     half = (x.double() / 2).to(dtype)
     wide = torch.empty(9, cols + 3, dtype=dtype, device="cuda")[:, 1:-2]
